@@ -189,9 +189,9 @@ def _new_cache(pages, case):
     return c
 
 
-def _handle(c):
+def _handle(c, dtype):
     import quantized_attention_08_b200 as sage
-    return sage.SageKVCache(c["k"], c["v"], c.get("k_scale"), c.get("v_scale"))
+    return sage.SageKVCache(c["k"], c["v"], c.get("k_scale"), c.get("v_scale"), dtype)
 
 
 def _ints(v):
@@ -273,7 +273,7 @@ def _inputs(case, seed):
 def prepare(case, seed):
     state = dict(_inputs(case, seed), case=case)
     if own and "cache" in state:
-        state["handle"] = _handle(state["cache"])  # a program keeps one for its cache
+        state["handle"] = _handle(state["cache"], DTYPES[case["dtype"]])  # a program keeps one for its cache
     return state
 
 
