@@ -282,6 +282,156 @@ sage_status_t sage_attn_fwd_varlen(const void* q, const void* k, const void* v, 
                                    int H_kv, int d, int causal, float sm_scale, int variant,
                                    void* stream);
 
+/*
+ * Serving from a paged key-value cache: what follows a prefill.  A step of a
+ * batch of requests is
+ *   sage_kv_slots   block tables and slot maps from the requests' lengths
+ *   sage_rope_axes  rotary positions of the step's Q and K
+ *   sage_kv_append  the step's K and V, smoothed and quantized, into the cache
+ *   sage_attn_decode_paged  attention of the new tokens over the cache
+ * (prompts attend through sage_attn_fwd_varlen, whose pre-pass also gives the
+ * mean_k that the cache's K is smoothed by).  These entry points take fp16 and
+ * bf16.  Lengths, tables, slots and positions are read on the device, so that
+ * a step can be captured in a CUDA graph and replayed as the requests grow.
+ * None of them allocates device memory or keeps state.
+ */
+typedef enum { SAGE_F16 = 0, SAGE_BF16 = 1 } sage_dtype_t;
+
+typedef enum {
+  SAGE_KV_16 = 0,   /* K and V in the 16-bit type                                     */
+  SAGE_KV_B = 1,    /* K int8 with one scale per token and head, V in the 16-bit type */
+  SAGE_KV_8P8 = 2   /* K int8, V FP8 E4M3, one scale per token and head each          */
+} sage_kv_format_t;
+
+/*
+ * A paged cache.  k and v are [num_pages, H_kv, page_size, d] with dense pages
+ * (a page's H_kv * page_size * d elements are contiguous), 16-byte aligned; the
+ * page strides, in elements, may be larger than a page (K and V pages in one
+ * allocation, say) and are multiples of 16 bytes.  k_scale and v_scale are
+ * fp32 [num_pages, H_kv, page_size] with their own page strides: K = code *
+ * k_scale, V = e4m3 * v_scale (unused ones are ignored and may be NULL).
+ * page_size is a multiple of 16, num_pages * page_size < 2^31.  Slot s is token
+ * s % page_size of page s / page_size.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t k_page_stride, v_page_stride, k_scale_page_stride, v_scale_page_stride;
+  int num_pages, page_size, H_kv, d;
+  int format; /* sage_kv_format_t */
+  int dtype;  /* sage_dtype_t: of the 16-bit parts, of the new K and V, and of Q and O */
+} sage_kv_cache_t;
+
+/*
+ * Block tables and slot maps of one step, from the requests' lengths.
+ *   ctx_lens : int32 [B] tokens of each request already cached
+ *   new_lens : int32 [B] tokens that the step adds
+ *   free_pages, num_free: pages that no request holds; the first *free_used
+ *              (int32 in device memory) of them are taken already
+ *   block_table: int32 [B, max_pages]; row b holds the pages of request b, the
+ *              first ceil(ctx / page_size) valid on entry.  Pages that the new
+ *              tokens need are taken from the free list in the order of the
+ *              requests and written behind them (-1 past the list's end); no
+ *              other entry is touched
+ *   seq_lens : int32 [B] = ctx + new, cut to the tokens that have a page
+ *   cu_seqlens: int32 [B+1]: the step's tokens are packed in the order of the
+ *              requests, those of request b at cu_seqlens[b] .. cu_seqlens[b+1]-1
+ *   slot_map, positions, seq_ids: int32 [T]: cache slot (-1 if its page could
+ *              not be had), position in its request and request of each packed
+ *              token; -1 in all three for the places behind the last token
+ *   free_used_out: int32, *free_used plus the pages taken (at most num_free)
+ * seq_lens may be ctx_lens and free_used_out may be free_used (a replayed
+ * step); other arrays must not overlap.  Lengths are cut to what the table's
+ * rows can hold and tokens to T; negative ones count as 0.  B <= 8192,
+ * max_pages * page_size < 2^31, T <= 2^30.
+ */
+sage_status_t sage_kv_slots(const int32_t* ctx_lens, const int32_t* new_lens, int B,
+                            const int32_t* free_pages, int num_free, const int32_t* free_used,
+                            int32_t* block_table, int max_pages, int page_size, int32_t* seq_lens,
+                            int32_t* cu_seqlens, int32_t* slot_map, int32_t* positions,
+                            int32_t* seq_ids, int T, int32_t* free_used_out, void* stream);
+
+/*
+ * Rotary positions with several axes (time, height, width, ...), Q and K in
+ * one launch.
+ *   q, q_out : [B, H, N, d], k, k_out: [B, H_kv, N, d] in `dtype`; element (b, h, n, c)
+ *              is at b * s[0] + h * s[1] + n * s[2] + c of its stride array (in
+ *              elements, HOST memory; multiples of 8).  k, k_out may both be NULL.
+ *              An output may be its input (same pointer and strides); otherwise
+ *              they must not overlap
+ *   positions: int32, axis a of token (b, n) at a * pos_strides[0] + b * pos_strides[1]
+ *              + n (pos_strides[1] = 0: shared by the batch)
+ *   sections : HOST int [n_axes], rotation pairs of each axis in turn; their sum R
+ *              is a multiple of 8 and at most d / 2; n_axes <= 4
+ *   inv_freq : fp32 [R]
+ * Pair i of axis a turns by theta = positions[a] * inv_freq[i], formed and
+ * reduced in fp64; cos and sin of the reduced angle, products and sums in fp32
+ * (each rounded to nearest), one rounding to `dtype`.  Pairs are channels
+ * (i, i + R), or (2i, 2i + 1) if `interleaved`; channels from 2R on are copied.
+ */
+sage_status_t sage_rope_axes(const void* q, const int64_t* q_strides, void* q_out,
+                             const int64_t* q_out_strides, const void* k, const int64_t* k_strides,
+                             void* k_out, const int64_t* k_out_strides, const int32_t* positions,
+                             const int64_t* pos_strides, const float* inv_freq, const int* sections,
+                             int n_axes, int B, int H, int H_kv, int N, int d, int interleaved,
+                             int dtype, void* stream);
+
+/*
+ * Writes T new tokens' K and V into the cache.
+ *   k, v     : [H_kv, T, d] in cache->dtype; element (h, t, c) at h * s[0] + t * s[1] + c
+ *              of its stride array (elements, HOST memory; multiples of 8), 16-byte aligned
+ *   slot_map : int32 [T]; tokens whose slot lies outside the cache (-1) are skipped.
+ *              The slots of one call are distinct (of a repeated one, which token's
+ *              parts end up in it is not defined)
+ *   mean_k   : fp32 [B, H_kv, d] or NULL, subtracted from K (one fp32 subtraction);
+ *              seq_ids: int32 [T], the row of mean_k of each token (tokens with one
+ *              outside [0, B) are skipped).  Smooth K per request: a softmax over a
+ *              request's keys does not change when one vector is taken off all of
+ *              them, so every token of a request has to use the same mean
+ * Quantization is per token and head (x = K minus its mean):
+ *   K: delta = max|x| * (1 / 127), code = RNE(x / delta)
+ *   V: delta = max|v| * (1 / 448), code = e4m3_rne_satfinite(v / delta)
+ * (the constants, the products and the divisions each rounded to fp32), with
+ * delta = 0 and codes 0 where delta would be below 2^-100.
+ */
+sage_status_t sage_kv_append(const void* k, const int64_t* k_strides, const void* v,
+                             const int64_t* v_strides, int T, const int32_t* slot_map,
+                             const float* mean_k, const int32_t* seq_ids, int B,
+                             const sage_kv_cache_t* cache, void* stream);
+
+/*
+ * Attention of n_q new tokens of each request over its cached tokens (the new
+ * ones among them: append first).
+ *   q        : [B, H, n_q, d] in cache->dtype; element (b, h, i, c) at b * s[0] + h * s[1]
+ *              + i * s[2] + c (elements, HOST memory; multiples of 8), 16-byte aligned
+ *   block_table: int32 [B, max_pages]; seq_lens: int32 [B], cached tokens of each
+ *              request (cut to [0, max_len]); max_len <= max_pages * page_size
+ *   causal   : 1: query i sees the keys t < len - n_q + i + 1 (the new tokens are the
+ *              last n_q of the cache); 0: all of them (cross attention, n_q = 1)
+ *   o        : dense [B, H, n_q, d]; rows that see no key are 0
+ *   lse      : NULL, or fp32 [B, H, n_q]: ln sum exp(score) (natural units, of the
+ *              cached, smoothed K), -infinity for rows that see no key
+ *   workspace: at least sage_attn_decode_workspace_bytes() bytes, 256-byte aligned
+ *              (NULL if that is 0); holds no state between calls, but calls that may
+ *              overlap need one each
+ * Tokens on a page outside the cache count as absent.  Entries of block_table
+ * behind a request's last page are not read, nor are slots behind its last
+ * token.  Results do not depend on what else runs, and two calls on the same
+ * inputs agree bit for bit.  B <= 4096, n_q * H / H_kv <= 1024.
+ */
+sage_status_t sage_attn_decode_paged(const void* q, const int64_t* q_strides,
+                                     const sage_kv_cache_t* cache, const int32_t* block_table,
+                                     int max_pages, const int32_t* seq_lens, int B, int H, int n_q,
+                                     int max_len, int causal, float sm_scale, void* o, float* lse,
+                                     void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace sage_attn_decode_paged needs for these sizes (0: none, or
+ * sizes it rejects). */
+size_t sage_attn_decode_workspace_bytes(int B, int H, int H_kv, int n_q, int d, int max_len,
+                                        int format);
+
 /* Layout of v_hat: 0 = [B,H_kv,N,d] (same as v).  Always 0 in this library. */
 int sage_v_hat_layout(void);
 

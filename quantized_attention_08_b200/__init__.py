@@ -14,10 +14,14 @@ Functions carry the names of the C entry points:
   sage_attn_fwd_varlen, sage_get_device_error, sage_set_wait_timeout_ns,
   sage_selftest_wait_timeout, sage_status_string, sage_version,
   sage_v_hat_layout.
+Serving from a paged key-value cache (SageKVCache holds one; fp16 and bf16):
+  sage_kv_slots, sage_rope_axes, sage_kv_append, sage_attn_decode_paged,
+  sage_attn_decode_workspace_bytes.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -56,6 +60,14 @@ _SIGS = {
                                             _i, _i, _i, _i, _vp]),
     "sage_attn_fwd_varlen": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i,
                                   _vp]),
+    "sage_kv_slots": (_i, [_vp, _vp, _i, _vp, _i, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp,
+                           _vp]),
+    "sage_rope_axes": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
+                            _i, _i, _i, _i, _vp]),
+    "sage_kv_append": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp]),
+    "sage_attn_decode_paged": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp,
+                                    _c.c_size_t, _vp]),
+    "sage_attn_decode_workspace_bytes": (_c.c_size_t, [_i, _i, _i, _i, _i, _i, _i]),
     "sage_v_hat_layout": (_i, []),
     "sage_get_device_error": (_i, [_vp, _c.POINTER(_c.c_uint32)]),
     "sage_set_wait_timeout_ns": (None, [_c.c_uint64]),
@@ -405,6 +417,325 @@ def sage_attn_fwd_varlen(q, k, v, cu_seqlens, max_seqlen: int, *, causal: bool =
         int(bool(causal)), float(sm_scale), _variant(variant), _stream(stream))
     _check(st, "sage_attn_fwd_varlen")
     return o
+
+
+# ------------------------------------------------- serving from a paged cache
+KV_FORMATS = {"16": 0, "B": 1, "8+8": 2}
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+_i64x2 = _c.c_int64 * 2
+_i64x3 = _c.c_int64 * 3
+
+
+class _CacheStruct(_c.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp),
+                ("k_page_stride", _c.c_int64), ("v_page_stride", _c.c_int64),
+                ("k_scale_page_stride", _c.c_int64), ("v_scale_page_stride", _c.c_int64),
+                ("num_pages", _i), ("page_size", _i), ("H_kv", _i), ("d", _i), ("format", _i),
+                ("dtype", _i)]
+
+
+# The serving calls of a decode step take microseconds on the GPU, so their
+# checks keep to cheap accessors: device numbers for devices, torch's raw
+# stream lookup, and each library function looked up once.
+def _serving(t: torch.Tensor, dtype, name: str, dev: int):
+    """Checks of a serving argument (type, device number, last axis dense);
+    returns its strides, 0 for an axis of one entry (never used, and torch
+    may say anything there)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    shape, st = t.shape, t.stride()
+    if 1 in shape:
+        st = [s if n > 1 else 0 for n, s in zip(shape, st)]
+        if shape and shape[-1] == 1:
+            st[-1] = 1
+    if shape and st[-1] != 1:
+        raise ValueError(f"{name} must be dense along its last axis")
+    return st
+
+
+def _ints(t: torch.Tensor, name: str, dev: int, shape) -> int:
+    """Checks of an int32 argument (type, device number, shape, contiguous);
+    returns its address."""
+    if t.dtype is not torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+_fns = {}
+
+
+def _call(name: str, dev: int, *args):
+    """Calls the library with device `dev` current, on its current stream."""
+    if dev < 0:
+        raise TypeError(f"{name} takes CUDA tensors")
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(load_library(), name)
+    st = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, st)
+    if status:
+        raise SageError(status, name)
+
+
+def _on_stream(f):
+    """A `stream` argument makes that stream current for the call, so that the
+    outputs and workspaces that torch hands out belong to it."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        dev = next(a.device for a in (*args, *kw.values()) if isinstance(a, torch.Tensor))
+        if not isinstance(stream, torch.cuda.Stream):
+            ptr = int(getattr(stream, "cuda_stream", stream))
+            stream = torch.cuda.ExternalStream(ptr, dev) if ptr else torch.cuda.default_stream(dev)
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
+
+
+class SageKVCache:
+    """A paged key-value cache: k and v [num_pages, H_kv, page_size, d], with
+    dense pages, and fp32 scales [num_pages, H_kv, page_size].  The format
+    follows from the types: "16" (k and v fp16 or bf16), "B" (k int8 with
+    k_scale, v 16-bit), "8+8" (k int8, v uint8 E4M3 codes, both scales; `dtype`
+    is that of the model, fp16 unless given).  The tensors are the caller's
+    and are used in place."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None, dtype: Optional[torch.dtype] = None):
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must both be [num_pages, H_kv, page_size, d]")
+        if k.dtype in _DTYPES and v.dtype == k.dtype:
+            self.format, model = "16", k.dtype
+        elif k.dtype == torch.int8 and v.dtype in _DTYPES:
+            self.format, model = "B", v.dtype
+        elif k.dtype == torch.int8 and v.dtype == torch.uint8:
+            self.format, model = "8+8", dtype or torch.float16
+        else:
+            raise TypeError(f"no cache format has k {k.dtype} and v {v.dtype}")
+        if model not in _DTYPES or (dtype is not None and dtype != model):
+            raise TypeError(f"dtype {dtype} does not fit k {k.dtype} and v {v.dtype}")
+        if not k.is_cuda:
+            raise TypeError("k must be a CUDA tensor")
+        self._dev = k.get_device()
+        self.k, self.v, self.dtype, self.device = k, v, model, k.device
+        self.k_scale = k_scale if self.format != "16" else None
+        self.v_scale = v_scale if self.format == "8+8" else None
+        self.num_pages, self.H_kv, self.page_size, self.d = k.shape
+        s = self._struct = _CacheStruct()
+        for name, t, inner in (("k", k, k.shape[1:]), ("v", v, k.shape[1:]),
+                               ("k_scale", self.k_scale, k.shape[1:3]),
+                               ("v_scale", self.v_scale, k.shape[1:3])):
+            if t is None:
+                if (name == "k_scale" and self.format != "16") or (name == "v_scale" and self.format == "8+8"):
+                    raise ValueError(f"a cache of format {self.format} needs {name}")
+                continue
+            if name.endswith("scale"):
+                _serving(t, torch.float32, name, self._dev)
+                if t.shape != k.shape[:3]:
+                    raise ValueError(f"{name} must be [num_pages, H_kv, page_size]")
+            elif t.device != self.device:
+                raise ValueError(f"{name} must be on {self.device}")
+            if self.num_pages and not t[0].is_contiguous():
+                raise ValueError(f"a page of {name} must be contiguous")
+            n = 1
+            for x in inner:
+                n *= x
+            setattr(s, name, t.data_ptr())
+            setattr(s, name + "_page_stride", t.stride(0) if self.num_pages > 1 else n)
+        s.num_pages, s.H_kv, s.page_size, s.d = k.shape
+        s.format, s.dtype = KV_FORMATS[self.format], _DTYPES[model]
+        self._ref = _c.addressof(s)
+
+    @classmethod
+    def allocate(cls, num_pages: int, H_kv: int, page_size: int, d: int, format: str = "8+8",
+                 dtype: torch.dtype = torch.float16, device="cuda"):
+        """A cache of zeros."""
+        if format not in KV_FORMATS:
+            raise ValueError(f"format must be one of {list(KV_FORMATS)}, got {format!r}")
+        shape = (num_pages, H_kv, page_size, d)
+        kt = dtype if format == "16" else torch.int8
+        vt = torch.uint8 if format == "8+8" else dtype
+        scale = lambda: torch.zeros(shape[:3], dtype=torch.float32, device=device)  # noqa: E731
+        return cls(torch.zeros(shape, dtype=kt, device=device), torch.zeros(shape, dtype=vt, device=device),
+                   scale() if format != "16" else None, scale() if format == "8+8" else None, dtype)
+
+
+@_on_stream
+def sage_kv_slots(ctx_lens, new_lens, free_pages, free_used, block_table, *, page_size: int, T: int,
+                  out=None):
+    """Block tables and slot maps of one step: ctx_lens, new_lens int32 [B],
+    free_pages int32 [F] of which the first free_used (int32 [1]) are taken,
+    block_table int32 [B, max_pages] (extended in place).  Returns (seq_lens
+    [B], cu_seqlens [B+1], slot_map [T], positions [T], seq_ids [T],
+    free_used [1]), all int32; `out` takes the same six tensors, of which
+    seq_lens may be ctx_lens and free_used its input."""
+    dev = ctx_lens.get_device()
+    B, F, width = ctx_lens.numel(), free_pages.numel(), block_table.shape[-1]
+    if out is None:
+        if T < 0:
+            raise ValueError("T must not be negative")
+        out = torch.empty(2 * B + 3 * T + 2, dtype=torch.int32, device=ctx_lens.device).split_with_sizes(
+            (B, B + 1, T, T, T, 1))
+        lens = out[0].data_ptr()
+        cu = lens + 4 * B
+        slots = cu + 4 * B + 4
+        pos, ids, used = slots + 4 * T, slots + 8 * T, slots + 12 * T
+    else:
+        lens, cu, slots, pos, ids, used = (
+            _ints(t, name, dev, (n,)) for t, name, n in
+            zip(out, ("seq_lens", "cu_seqlens", "slot_map", "positions", "seq_ids", "free_used"),
+                (B, B + 1, T, T, T, 1)))
+    _call("sage_kv_slots", dev, _ints(ctx_lens, "ctx_lens", dev, (B,)), _ints(new_lens, "new_lens", dev, (B,)), B,
+          _ints(free_pages, "free_pages", dev, (F,)), F, _ints(free_used, "free_used", dev, (1,)),
+          _ints(block_table, "block_table", dev, (B, width)), width, page_size, lens, cu, slots, pos, ids, T, used)
+    return out
+
+
+@_on_stream
+def sage_rope_axes(q, k, positions, inv_freq, sections, *, pairing: str = "half", q_out=None, k_out=None):
+    """Rotary positions with several axes of q [B, H, N, d] and k [B, H_kv, N, d]
+    (or [H, N, d] of one sequence; k may be None), any strides with a dense
+    last axis.  positions int32 [axes, B, N] or [axes, N] (shared by the batch);
+    sections: rotation pairs of each axis; inv_freq fp32 [sum(sections)];
+    pairing "half" (i, i + R) or "interleaved" (2i, 2i + 1).  Returns (q, k)
+    rotated; q_out / k_out take them instead (they may be q and k)."""
+    dtype = q.dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"q must be torch.float16 or torch.bfloat16, got {dtype}")
+    if pairing not in ("half", "interleaved"):
+        raise ValueError(f"pairing must be 'half' or 'interleaved', got {pairing!r}")
+    dev = q.get_device()
+    shape = q.shape
+    if len(shape) not in (3, 4):
+        raise ValueError("q must be [B, H, N, d] or [H, N, d]")
+    B = shape[0] if len(shape) == 4 else 1
+    H, N, d = shape[-3:]
+
+    def s3(t, like, name):
+        if t.shape != like:
+            raise ValueError(f"{name} does not have the shape of its input")
+        st = _serving(t, dtype, name, dev)
+        return _i64x3(*st[:3]) if len(st) == 4 else _i64x3(0, st[0], st[1])
+
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=dtype, device=q.device)
+    Hk, kp, kop, ks, kos = 0, None, None, None, None
+    if k is not None:
+        kshape = k.shape
+        if len(kshape) != len(shape) or kshape[-2:] != shape[-2:] or kshape[:-3] != shape[:-3]:
+            raise ValueError("q and k must have the same batch, tokens and channels")
+        if k_out is None:
+            k_out = torch.empty(kshape, dtype=dtype, device=q.device)
+        Hk, kp, kop = kshape[-3], k.data_ptr(), k_out.data_ptr()
+        ks, kos = s3(k, kshape, "k"), s3(k_out, kshape, "k_out")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    A, R = len(sections), sum(sections)
+    ps = _serving(positions, torch.int32, "positions", dev)
+    if positions.shape != (A, B, N) and positions.shape != (A, N):
+        raise ValueError(f"positions must be [{A}, {N}] or [{A}, {B}, {N}], got {tuple(positions.shape)}")
+    _serving(inv_freq, torch.float32, "inv_freq", dev)
+    if inv_freq.shape != (R,):
+        raise ValueError(f"inv_freq must have {R} entries")
+    qs, qos = s3(q, shape, "q"), s3(q_out, shape, "q_out")
+    _call("sage_rope_axes", dev, q.data_ptr(), qs, q_out.data_ptr(), qos, kp, ks, kop, kos, positions.data_ptr(),
+          _i64x2(ps[0], ps[1] if len(ps) == 3 else 0), inv_freq.data_ptr(), (_i * A)(*sections), A, B, H, Hk, N, d,
+          pairing == "interleaved", code)
+    return q_out, k_out
+
+
+@_on_stream
+def sage_kv_append(k, v, slot_map, cache: SageKVCache, *, mean_k=None, seq_ids=None):
+    """Writes new K and V [H_kv, T, d] (any strides with a dense last axis) into
+    the cache's slots slot_map int32 [T] (-1: skipped), quantized as the cache
+    holds them.  mean_k fp32 [B, H_kv, d] with seq_ids int32 [T]: subtracted
+    from K (Smooth K per request; every token of a request needs the same)."""
+    dev, shape = cache._dev, k.shape
+    ks, vs = _serving(k, cache.dtype, "k", dev), _serving(v, cache.dtype, "v", dev)
+    if len(shape) != 3 or v.shape != shape or shape[0] != cache.H_kv or shape[2] != cache.d:
+        raise ValueError(f"k and v must both be [{cache.H_kv}, T, {cache.d}]")
+    T = shape[1]
+    B, mean, ids = 0, None, None
+    if mean_k is not None:
+        if seq_ids is None:
+            raise ValueError("mean_k needs seq_ids")
+        _serving(mean_k, torch.float32, "mean_k", dev)
+        B = mean_k.shape[0]
+        if mean_k.shape != (B, cache.H_kv, cache.d) or not mean_k.is_contiguous():
+            raise ValueError(f"mean_k must be contiguous [B, {cache.H_kv}, {cache.d}]")
+        mean, ids = mean_k.data_ptr(), _ints(seq_ids, "seq_ids", dev, (T,))
+    _call("sage_kv_append", dev, k.data_ptr(), _i64x2(ks[0], ks[1]), v.data_ptr(), _i64x2(vs[0], vs[1]), T,
+          _ints(slot_map, "slot_map", dev, (T,)), mean, ids, B, cache._ref)
+    return cache
+
+
+def sage_attn_decode_workspace_bytes(B: int, H: int, H_kv: int, n_q: int, d: int, max_len: int,
+                                     format="8+8") -> int:
+    return load_library().sage_attn_decode_workspace_bytes(
+        B, H, H_kv, n_q, d, max_len, KV_FORMATS[format] if isinstance(format, str) else int(format))
+
+
+@_on_stream
+def sage_attn_decode_paged(q, cache: SageKVCache, block_table, seq_lens, max_len: int, *,
+                           causal: bool = True, sm_scale: Optional[float] = None, o=None,
+                           return_lse: bool = False, workspace: Optional[torch.Tensor] = None):
+    """Attention of new tokens over the paged cache: q [B, H, n_q, d], or
+    [B, H, d] of one token, any strides with a dense last axis; block_table
+    int32 [B, max_pages], seq_lens int32 [B] (the new tokens included), max_len
+    a bound on them.  causal: query i sees the keys up to its own token (the
+    last n_q are the new ones).  Returns o (dense, q's shape), or (o, lse fp32)
+    with return_lse.  workspace: a tensor of at least
+    sage_attn_decode_workspace_bytes() bytes; taken from torch if not given."""
+    dev, d, shape = cache._dev, cache.d, q.shape
+    qs = _serving(q, cache.dtype, "q", dev)
+    if len(shape) == 4:
+        B, H, n_q, dq = shape
+        qs = _i64x3(qs[0], qs[1], qs[2])
+    elif len(shape) == 3:
+        B, H, dq = shape
+        n_q, qs = 1, _i64x3(qs[0], qs[1], 0)
+    else:
+        dq = -1
+    if dq != d:
+        raise ValueError(f"q must be [B, H, n_q, {d}] or [B, H, {d}]")
+    width = block_table.shape[-1]
+    if o is None:
+        o = torch.empty(shape, dtype=q.dtype, device=q.device)
+    else:
+        _serving(o, q.dtype, "o", dev)
+        if o.shape != shape or not o.is_contiguous():
+            raise ValueError("o must be contiguous and have q's shape")
+    lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device) if return_lse else None
+    if workspace is None:
+        size = sage_attn_decode_workspace_bytes(B, H, cache.H_kv, n_q, d, max_len, cache._struct.format)
+        ws = None
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    else:
+        ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call("sage_attn_decode_paged", dev, q.data_ptr(), qs, cache._ref,
+          _ints(block_table, "block_table", dev, (B, width)), width, _ints(seq_lens, "seq_lens", dev, (B,)), B, H, n_q,
+          max_len, bool(causal), 1.0 / math.sqrt(d) if sm_scale is None else sm_scale, o.data_ptr(), _ptr(lse), ws,
+          size)
+    return (o, lse) if return_lse else o
 
 
 def sage_get_device_error(stream=None):

@@ -12,8 +12,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsage.so")
-SOURCES = ["prepass.cu", "attn_sm100.cu", "sage_api.cu"]
-HEADERS = ["sage_ptx.cuh", "sage_internal.h", "quant_div.h", "quant_pair.cuh"]
+SOURCES = ["prepass.cu", "attn_sm100.cu", "kvcache.cu", "rope_axes.cu", "attn_decode.cu", "sage_api.cu"]
+HEADERS = ["sage_ptx.cuh", "sage_internal.h", "serve_internal.h", "quant_div.h", "quant_pair.cuh"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",

@@ -7,6 +7,7 @@
 
 #include "sage.h"
 #include "sage_internal.h"
+#include "serve_internal.h"
 
 namespace {
 
@@ -180,6 +181,41 @@ sage_status_t check_fwd_args(const void* q, const void* k, const void* v, void* 
   if (B == 0 || N == 0) return SAGE_OK;
   if (!q || !k || !v || !o) return SAGE_ERR_INVALID_ARG;
   if (!a16(q) || !a16(k) || !a16(v) || !a16(o)) return SAGE_ERR_MISALIGNED;
+  return SAGE_OK;
+}
+
+// A paged cache's sizes, strides and pointers.
+sage_status_t check_cache(const sage_kv_cache_t* c) {
+  if (!c) return SAGE_ERR_INVALID_ARG;
+  if (c->num_pages < 0 || c->page_size <= 0 || c->H_kv <= 0) return SAGE_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return SAGE_ERR_UNSUPPORTED;
+  if (c->format != SAGE_KV_16 && c->format != SAGE_KV_B && c->format != SAGE_KV_8P8)
+    return SAGE_ERR_UNSUPPORTED;
+  if (c->dtype != SAGE_F16 && c->dtype != SAGE_BF16) return SAGE_ERR_UNSUPPORTED;
+  if (c->page_size % 16 != 0 || c->H_kv > 65535) return SAGE_ERR_UNSUPPORTED;
+  if (static_cast<long long>(c->num_pages) * c->page_size > 0x7fffffffll) return SAGE_ERR_UNSUPPORTED;
+  if (c->num_pages == 0) return SAGE_OK;
+  const bool ks = c->format != SAGE_KV_16, vs = c->format == SAGE_KV_8P8;
+  if (!c->k || !c->v || (ks && !c->k_scale) || (vs && !c->v_scale)) return SAGE_ERR_INVALID_ARG;
+  const int64_t rows = static_cast<int64_t>(c->H_kv) * c->page_size;
+  if (c->k_page_stride < rows * c->d || c->v_page_stride < rows * c->d ||
+      (ks && c->k_scale_page_stride < rows) || (vs && c->v_scale_page_stride < rows))
+    return SAGE_ERR_INVALID_ARG;
+  if (!a16(c->k) || !a16(c->v) || (ks && !a4(c->k_scale)) || (vs && !a4(c->v_scale)) ||
+      c->k_page_stride % (ks ? 16 : 8) != 0 || c->v_page_stride % (vs ? 16 : 8) != 0)
+    return SAGE_ERR_MISALIGNED;
+  return SAGE_OK;
+}
+
+sage_status_t check_decode_sizes(int B, int H, int H_kv, int n_q, int d, int max_len, int format) {
+  if (B < 0 || H <= 0 || H_kv <= 0 || n_q < 0 || max_len < 0) return SAGE_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return SAGE_ERR_UNSUPPORTED;
+  if (H % H_kv != 0) return SAGE_ERR_UNSUPPORTED;
+  if (format != SAGE_KV_16 && format != SAGE_KV_B && format != SAGE_KV_8P8) return SAGE_ERR_UNSUPPORTED;
+  if (B > 4096 || static_cast<long long>(n_q) * (H / H_kv) > 1024) return SAGE_ERR_UNSUPPORTED;
+  // steps of at least 16 tokens are counted in 32 bits
+  if (static_cast<long long>(B) * ((max_len + 15ll) / 16) > 0x7fffffffll) return SAGE_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * H * (n_q > 0 ? n_q : 1) > 0x7fffffffll) return SAGE_ERR_UNSUPPORTED;
   return SAGE_OK;
 }
 
@@ -752,6 +788,181 @@ sage_status_t sage_attn_fwd_varlen(const void* q, const void* k, const void* v, 
   cudaError_t ef = cudaFreeAsync(ws, st);
   if (s != SAGE_OK) return s;
   return from_cuda(ef);
+}
+
+sage_status_t sage_kv_slots(const int32_t* ctx_lens, const int32_t* new_lens, int B,
+                            const int32_t* free_pages, int num_free, const int32_t* free_used,
+                            int32_t* block_table, int max_pages, int page_size, int32_t* seq_lens,
+                            int32_t* cu_seqlens, int32_t* slot_map, int32_t* positions,
+                            int32_t* seq_ids, int T, int32_t* free_used_out, void* stream) {
+  if (B < 0 || num_free < 0 || max_pages < 0 || page_size <= 0 || T < 0) return SAGE_ERR_INVALID_ARG;
+  if (B > 8192 || T > (1 << 30) || static_cast<long long>(max_pages) * page_size > 0x7fffffffll)
+    return SAGE_ERR_UNSUPPORTED;
+  if (!cu_seqlens || !free_used || !free_used_out) return SAGE_ERR_INVALID_ARG;
+  if (B > 0 && (!ctx_lens || !new_lens || !seq_lens || (max_pages > 0 && !block_table)))
+    return SAGE_ERR_INVALID_ARG;
+  if (num_free > 0 && !free_pages) return SAGE_ERR_INVALID_ARG;
+  if (T > 0 && (!slot_map || !positions || !seq_ids)) return SAGE_ERR_INVALID_ARG;
+  if (!a4(ctx_lens) || !a4(new_lens) || !a4(free_pages) || !a4(free_used) || !a4(block_table) ||
+      !a4(seq_lens) || !a4(cu_seqlens) || !a4(slot_map) || !a4(positions) || !a4(seq_ids) ||
+      !a4(free_used_out))
+    return SAGE_ERR_MISALIGNED;
+  sage_status_t s = check_device();
+  if (s != SAGE_OK) return s;
+  sage::SlotArgs a;
+  a.ctx_lens = ctx_lens;
+  a.new_lens = new_lens;
+  a.free_pages = free_pages;
+  a.free_used = free_used;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.cu_seqlens = cu_seqlens;
+  a.slot_map = slot_map;
+  a.positions = positions;
+  a.seq_ids = seq_ids;
+  a.free_used_out = free_used_out;
+  a.B = B;
+  a.num_free = num_free;
+  a.max_pages = max_pages;
+  a.page_size = page_size;
+  a.T = T;
+  return from_cuda(sage::launch_kv_slots(a, static_cast<cudaStream_t>(stream)));
+}
+
+sage_status_t sage_rope_axes(const void* q, const int64_t* q_strides, void* q_out,
+                             const int64_t* q_out_strides, const void* k, const int64_t* k_strides,
+                             void* k_out, const int64_t* k_out_strides, const int32_t* positions,
+                             const int64_t* pos_strides, const float* inv_freq, const int* sections,
+                             int n_axes, int B, int H, int H_kv, int N, int d, int interleaved,
+                             int dtype, void* stream) {
+  const bool hk = k != nullptr;
+  if (B < 0 || H <= 0 || N < 0 || (hk && H_kv <= 0) || n_axes <= 0 || !sections)
+    return SAGE_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return SAGE_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || n_axes > sage::kMaxAxes || (dtype != SAGE_F16 && dtype != SAGE_BF16))
+    return SAGE_ERR_UNSUPPORTED;
+  sage::RopeArgs a = {};
+  for (int i = 0; i < n_axes; ++i) {
+    if (sections[i] < 0 || sections[i] > d / 2) return SAGE_ERR_INVALID_ARG;
+    a.pairs += sections[i];
+    a.sec_end[i] = a.pairs;
+  }
+  if (a.pairs == 0 || a.pairs > d / 2) return SAGE_ERR_INVALID_ARG;
+  if (a.pairs % 8 != 0) return SAGE_ERR_UNSUPPORTED;
+  // grid.x counts groups of at least 32 tokens, grid.y groups of heads
+  if (static_cast<long long>(B) * N > (1ll << 35) || H + (hk ? H_kv : 0) > 65535)
+    return SAGE_ERR_UNSUPPORTED;
+  if (B == 0 || N == 0) return SAGE_OK;
+  if (!q || !q_out || !q_strides || !q_out_strides || !positions || !pos_strides || !inv_freq)
+    return SAGE_ERR_INVALID_ARG;
+  if (hk != (k_out != nullptr) || (hk && (!k_strides || !k_out_strides))) return SAGE_ERR_INVALID_ARG;
+  if (!a16(q) || !a16(q_out) || !a16(k) || !a16(k_out) || !a4(positions) || !a4(inv_freq))
+    return SAGE_ERR_MISALIGNED;
+  a.in[0] = q;
+  a.out[0] = q_out;
+  a.in[1] = k;
+  a.out[1] = k_out;
+  a.heads[0] = H;
+  a.heads[1] = hk ? H_kv : 0;
+  for (int w = 0; w < (hk ? 2 : 1); ++w)
+    for (int i = 0; i < 3; ++i) {
+      a.in_s[w][i] = (w ? k_strides : q_strides)[i];
+      a.out_s[w][i] = (w ? k_out_strides : q_out_strides)[i];
+      if (a.in_s[w][i] % 8 != 0 || a.out_s[w][i] % 8 != 0) return SAGE_ERR_MISALIGNED;
+    }
+  a.pos = positions;
+  a.pos_s[0] = pos_strides[0];
+  a.pos_s[1] = pos_strides[1];
+  a.inv_freq = inv_freq;
+  a.axes = n_axes;
+  a.B = B;
+  a.N = N;
+  a.d = d;
+  a.interleaved = interleaved;
+  a.bf16 = dtype == SAGE_BF16;
+  sage_status_t s = check_device();
+  if (s != SAGE_OK) return s;
+  return from_cuda(sage::launch_rope_axes(a, static_cast<cudaStream_t>(stream)));
+}
+
+sage_status_t sage_kv_append(const void* k, const int64_t* k_strides, const void* v,
+                             const int64_t* v_strides, int T, const int32_t* slot_map,
+                             const float* mean_k, const int32_t* seq_ids, int B,
+                             const sage_kv_cache_t* cache, void* stream) {
+  sage_status_t s = check_cache(cache);
+  if (s != SAGE_OK) return s;
+  if (T < 0 || (mean_k && B < 0)) return SAGE_ERR_INVALID_ARG;
+  if (T > (1 << 30)) return SAGE_ERR_UNSUPPORTED;
+  if (T == 0) return SAGE_OK;
+  if (!k || !v || !k_strides || !v_strides || !slot_map || (mean_k && !seq_ids))
+    return SAGE_ERR_INVALID_ARG;
+  if (!a16(k) || !a16(v) || !a4(slot_map) || !a16(mean_k) || !a4(seq_ids)) return SAGE_ERR_MISALIGNED;
+  sage::AppendArgs a = {};
+  for (int i = 0; i < 2; ++i) {
+    a.in_s[0][i] = k_strides[i];
+    a.in_s[1][i] = v_strides[i];
+    if (k_strides[i] % 8 != 0 || v_strides[i] % 8 != 0) return SAGE_ERR_MISALIGNED;
+  }
+  a.in[0] = k;
+  a.in[1] = v;
+  a.slot_map = slot_map;
+  a.mean_k = mean_k;
+  a.seq_ids = seq_ids;
+  a.T = T;
+  a.B = B;
+  a.c = *cache;
+  if ((s = check_device()) != SAGE_OK) return s;
+  return from_cuda(sage::launch_kv_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sage_attn_decode_workspace_bytes(int B, int H, int H_kv, int n_q, int d, int max_len,
+                                        int format) {
+  if (check_decode_sizes(B, H, H_kv, n_q, d, max_len, format) != SAGE_OK || B == 0 || n_q == 0) return 0;
+  return sage::decode_workspace_bytes(B, H, H_kv, n_q, d, max_len, format);
+}
+
+sage_status_t sage_attn_decode_paged(const void* q, const int64_t* q_strides,
+                                     const sage_kv_cache_t* cache, const int32_t* block_table,
+                                     int max_pages, const int32_t* seq_lens, int B, int H, int n_q,
+                                     int max_len, int causal, float sm_scale, void* o, float* lse,
+                                     void* workspace, size_t ws_bytes, void* stream) {
+  sage_status_t s = check_cache(cache);
+  if (s != SAGE_OK) return s;
+  if ((s = check_decode_sizes(B, H, cache->H_kv, n_q, cache->d, max_len, cache->format)) != SAGE_OK) return s;
+  if (max_pages < 0 || static_cast<long long>(max_pages) * cache->page_size < max_len)
+    return SAGE_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return SAGE_ERR_INVALID_ARG;
+  if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return SAGE_ERR_INVALID_ARG;
+  if (B == 0 || n_q == 0) return SAGE_OK;
+  if (!q || !q_strides || !seq_lens || !o || (max_pages > 0 && !block_table)) return SAGE_ERR_INVALID_ARG;
+  if (!a16(q) || !a16(o) || !a4(block_table) || !a4(seq_lens) || !a4(lse)) return SAGE_ERR_MISALIGNED;
+  sage::DecodeArgs a = {};
+  for (int i = 0; i < 3; ++i) {
+    a.q_s[i] = q_strides[i];
+    if (q_strides[i] % 8 != 0) return SAGE_ERR_MISALIGNED;
+  }
+  const size_t need = sage::decode_workspace_bytes(B, H, cache->H_kv, n_q, cache->d, max_len, cache->format);
+  if (need > 0) {
+    if (ws_bytes < need) return SAGE_ERR_NO_MEMORY;
+    if (!workspace) return SAGE_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return SAGE_ERR_MISALIGNED;
+  }
+  a.q = q;
+  a.c = *cache;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.o = o;
+  a.lse = lse;
+  a.ws = workspace;
+  a.max_pages = max_pages;
+  a.B = B;
+  a.H = H;
+  a.n_q = n_q;
+  a.max_len = max_len;
+  a.causal = causal;
+  a.sm_scale = sm_scale;
+  if ((s = check_device()) != SAGE_OK) return s;
+  return from_cuda(sage::launch_attn_decode(a, static_cast<cudaStream_t>(stream)));
 }
 
 int sage_v_hat_layout(void) { return 0; }

@@ -1,0 +1,72 @@
+// serve_internal.h -- declarations of the serving kernels (paged cache,
+// rotary positions, decode attention) shared with the C entry points.
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "sage.h"
+
+namespace sage {
+
+struct SlotArgs {
+  const int32_t* ctx_lens;
+  const int32_t* new_lens;
+  const int32_t* free_pages;
+  const int32_t* free_used;  // may alias free_used_out
+  int32_t* block_table;
+  int32_t* seq_lens;         // may alias ctx_lens
+  int32_t* cu_seqlens;
+  int32_t* slot_map;
+  int32_t* positions;
+  int32_t* seq_ids;
+  int32_t* free_used_out;
+  int B, num_free, max_pages, page_size, T;
+};
+cudaError_t launch_kv_slots(const SlotArgs& a, cudaStream_t st);
+
+constexpr int kMaxAxes = 4;
+
+struct RopeArgs {
+  const void* in[2];      // q, k (k may be nullptr)
+  void* out[2];
+  int64_t in_s[2][3];     // strides of batch, head, token (elements)
+  int64_t out_s[2][3];
+  int heads[2];
+  const int32_t* pos;     // pos[a * pos_s[0] + b * pos_s[1] + n]
+  int64_t pos_s[2];
+  const float* inv_freq;  // [pairs]
+  int sec_end[kMaxAxes];  // pair i belongs to the first axis a with i < sec_end[a]
+  int axes, pairs;
+  int B, N, d;
+  int interleaved, bf16;
+};
+cudaError_t launch_rope_axes(const RopeArgs& a, cudaStream_t st);
+
+struct AppendArgs {
+  const void* in[2];     // k, v
+  int64_t in_s[2][2];    // strides of head, token (elements)
+  const int32_t* slot_map;
+  const float* mean_k;   // [B, H_kv, d] or nullptr
+  const int32_t* seq_ids;
+  int T, B;
+  sage_kv_cache_t c;
+};
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t st);
+
+struct DecodeArgs {
+  const void* q;
+  int64_t q_s[3];        // strides of batch, head, query token (elements)
+  sage_kv_cache_t c;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  void* o;
+  float* lse;            // or nullptr
+  void* ws;
+  int max_pages, B, H, n_q, max_len, causal;
+  float sm_scale;
+};
+size_t decode_workspace_bytes(int B, int H, int H_kv, int n_q, int d, int max_len, int format);
+cudaError_t launch_attn_decode(const DecodeArgs& a, cudaStream_t st);
+
+}  // namespace sage
