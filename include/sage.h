@@ -308,8 +308,9 @@ typedef enum {
  * (a page's H_kv * page_size * d elements are contiguous), 16-byte aligned; the
  * page strides, in elements, may be larger than a page (K and V pages in one
  * allocation, say) and are multiples of 16 bytes.  k_scale and v_scale are
- * fp32 [num_pages, H_kv, page_size] with their own page strides: K = code *
- * k_scale, V = e4m3 * v_scale (unused ones are ignored and may be NULL).
+ * fp32 [num_pages, H_kv, page_size] with their own page strides (16-byte
+ * aligned too, strides multiples of 4): K = code * k_scale, V = e4m3 * v_scale
+ * (unused ones are ignored and may be NULL).
  * page_size is a multiple of 16, num_pages * page_size < 2^31.  Slot s is token
  * s % page_size of page s / page_size.
  */

@@ -15,11 +15,12 @@
 // inside one warp's stretch is finished there; the pieces of the others go to
 // the workspace as (m, l, o) and a second kernel joins them in a fixed order.
 //
-// Loads.  A warp feeds its own ring in shared memory by cp.async, and every
-// lane copies exactly the bytes that it will read back, already in the order
-// of the MMA fragments -- so the ring needs no barrier and no swizzle, rows
-// of any page go through one path, and a masked row is a copy of zero bytes
-// (zero fill: a stale NaN behind the last token never reaches an MMA).
+// Loads.  One lane of a warp feeds the warp's own ring in shared memory with
+// bulk copies of whole rows (a step of a page is one run of memory for each of
+// K, V and the scales), counted by an mbarrier a stage; no other warp is
+// involved.  cp.async by the lanes that later read the bytes, in fragment order,
+// reached 4.9 TB/s where rows in order reach 6.5 (eight lanes then touch two
+// to four lines at once).
 //
 // Products.  mma.sync m16n8k16, transposed: S^T = K q^T and O^T = V^T P^T,
 // with tokens (channels) on the 16 side and query rows on the 8 side, since
@@ -39,6 +40,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "sage_ptx.cuh"
 #include "serve_internal.h"
 
 namespace sage {
@@ -71,6 +73,7 @@ struct DecodeParams {
   int B, H, Hk, G, n_q, rows, groups;  // rows = G * n_q in `groups` groups of 8 NT
   int max_len, causal, workers;
   float scale_log2;
+  uint64_t timeout_ns;
 };
 
 // ------------------------------------------------------------ types
@@ -78,14 +81,14 @@ template <typename T>
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1);
 template <>
 __device__ __forceinline__ void mma16816<__half>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 template <>
 __device__ __forceinline__ void mma16816<__nv_bfloat16>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -176,37 +179,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// cp.async of `BYTES` per lane; with ok == false the destination is zeroed
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool ok) {
-  const int n = ok ? BYTES : 0;
-  if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else if (BYTES == 8)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 r;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
-  return r;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 r;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
-  return r;
-}
-__device__ __forceinline__ float lds32(uint32_t a) {
-  float r;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(a));
-  return r;
+// Bulk copy of n bytes (a multiple of 16; both addresses 16-byte aligned),
+// counted by `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t n, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(n), "r"(smem_u32(bar))
+               : "memory");
 }
 
 // -------------------------------------------------------- shapes of a step
@@ -214,20 +192,22 @@ template <int D, int FMT>
 struct Step {
   static constexpr int KB = FMT == SAGE_KV_16 ? 2 : 1;   // bytes of a K element
   static constexpr int VB = FMT == SAGE_KV_8P8 ? 1 : 2;
-  static constexpr int KC = D * KB / 64;                 // 16-byte pieces of a lane's K row (4 lanes a row)
-  static constexpr int VW = D * VB / 8 < 16 ? 8 : 16;    // bytes of a lane's piece of a V row (8 lanes a row)
-  static constexpr int VC = D * VB / (8 * VW);
+  static constexpr int KROW = D * KB, VROW = D * VB;     // bytes of a row
+  static constexpr int KC = KROW / 64;                   // 16-byte pieces of a lane's K row (4 lanes a row)
+  static constexpr int VW = VROW / 8 < 16 ? 8 : 16;      // bytes of a lane's piece of a V row (8 lanes a row)
+  static constexpr int VC = VROW / (8 * VW);
   static constexpr int VE = VW / VB;                     // channels of a piece
   static constexpr bool KS = FMT != SAGE_KV_16;
   static constexpr bool VS = FMT == SAGE_KV_8P8;
   // 16-token tiles of a step: about 8 KB a step
   static constexpr int SUB = D == 128 ? (FMT == SAGE_KV_8P8 ? 2 : 1) : (FMT == SAGE_KV_8P8 ? 4 : 2);
   static constexpr int TOK = 16 * SUB;
-  static constexpr int K_BYTES = 2 * KC * 512;           // of a 16-token tile
-  static constexpr int V_BYTES = 4 * VC * VW * 32;
-  static constexpr int S_BYTES = (KS ? 64 : 0) + (VS ? 64 : 0);
-  static constexpr int TILE = K_BYTES + V_BYTES + S_BYTES;
-  static constexpr int STAGE = (SUB * TILE + 16 + 127) / 128 * 128;  // and a word of page flags
+  // a stage of the ring: K rows, V rows, K scales, V scales
+  static constexpr int V_AT = TOK * KROW;
+  static constexpr int KS_AT = V_AT + TOK * VROW;
+  static constexpr int VS_AT = KS_AT + (KS ? TOK * 4 : 0);
+  static constexpr int STAGE = VS_AT + (VS ? TOK * 4 : 0);
+  static constexpr int TOKEN = KROW + VROW + (KS ? 4 : 0) + (VS ? 4 : 0);  // bytes of a token
 };
 
 inline __host__ __device__ int steps_of(int len, int tok) { return (len + tok - 1) / tok; }
@@ -254,7 +234,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
   const int HZ = p.Hk * p.groups;
-  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * (kStages * S::STAGE);
+  uint8_t* const ring = smem + warp * (kStages * S::STAGE);
+  __shared__ __align__(8) uint64_t s_bar[kWarps][kStages];
+  __shared__ int s_abort[kWarps];
+  uint64_t* const bar = s_bar[warp];
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) mbar_init(bar + i, 1);
+    s_abort[warp] = 0;
+    fence_mbar_init();
+  }
+  __syncwarp();
   int* s_prefix = reinterpret_cast<int*>(smem + kWarps * kStages * S::STAGE);  // SPLIT only: [B + 1]
 
   // ---- this warp's stretch [at, end) of the line
@@ -328,83 +318,79 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
   };
   seek();
 
+  uint32_t absent = 0;  // 4 bits a stage: tiles on no page
+  // The page of the next tile; page tables are read 32 entries at a time.
+  auto next_page = [&]() {
+    if (page_base < 0 || tile_page >= page_base + 32) {
+      page_base = tile_page;
+      const int i = page_base + lane;
+      page_ids = i < p.max_pages && static_cast<int64_t>(i) * p.page_size < iss.len
+                     ? p.table[static_cast<int64_t>(iss.b) * p.max_pages + i]
+                     : -1;
+    }
+    return __shfl_sync(0xffffffffu, page_ids, tile_page - page_base);
+  };
+  // Copies of n tokens from offset tile_off of `page` to row `at` of a stage.
+  auto copy = [&](uint8_t* stage, uint64_t* b, int page, int at, int n) {
+    const int64_t in_page = static_cast<int64_t>(iss.z / p.groups) * p.page_size + tile_off;
+    const uint32_t dst = smem_u32(stage);
+    bulk_load(dst + at * S::KROW, p.k + page * p.k_page + in_page * S::KROW, n * S::KROW, b);
+    bulk_load(dst + S::V_AT + at * S::VROW, p.v + page * p.v_page + in_page * S::VROW, n * S::VROW, b);
+    if (S::KS) bulk_load(dst + S::KS_AT + at * 4, p.ks + page * p.ks_page + in_page, n * 4, b);
+    if (S::VS) bulk_load(dst + S::VS_AT + at * 4, p.vs + page * p.vs_page + in_page, n * 4, b);
+  };
   auto issue = [&](int slot) {
-    const uint32_t base = ring + slot * S::STAGE;
-    if (iss_left > 0) {
-      const int h = iss.z / p.groups;
-      const int32_t* row = p.table + static_cast<int64_t>(iss.b) * p.max_pages;
-      uint32_t bad = 0;
+    if (iss_left <= 0) return;
+    uint8_t* const stage = ring + slot * S::STAGE;
+    uint32_t gone = 0;
+    if (p.page_size % S::TOK == 0) {  // a step lies in one page
+      const int page = next_page();
+      const bool good = page >= 0 && page < p.num_pages;
+      if (!good) gone = (1u << S::SUB) - 1;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar + slot, good ? S::TOK * S::TOKEN : 0);
+        if (good) copy(stage, bar + slot, page, 0, S::TOK);
+      }
+      tile_off += S::TOK;
+      if (tile_off == p.page_size) {
+        tile_off = 0;
+        ++tile_page;
+      }
+    } else {
 #pragma unroll
       for (int s = 0; s < S::SUB; ++s) {
-        const int t0 = iss.step * S::TOK + 16 * s;
-        const int left = iss.len - t0;  // tokens of this tile and after it
-        int page = 0;
-        if (left > 0) {
-          if (page_base < 0 || tile_page >= page_base + 32) {
-            page_base = tile_page;
-            const int i = page_base + lane;
-            page_ids = i < p.max_pages && static_cast<int64_t>(i) * p.page_size < iss.len ? row[i] : -1;
-          }
-          page = __shfl_sync(0xffffffffu, page_ids, tile_page - page_base);
-        }
-        const bool good = left > 0 && page >= 0 && page < p.num_pages;
-        if (!good) {
-          bad |= 1u << s;
-          page = 0;
-        }
-        const int64_t in_page = static_cast<int64_t>(h) * p.page_size + tile_off;
-        const uint8_t* kp = p.k + page * p.k_page + in_page * (D * S::KB);
-        const uint8_t* vp = p.v + page * p.v_page + in_page * (D * S::VB);
-        const uint32_t dst = base + s * S::TILE;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const bool ok = good && j * 8 + g < left;
-          const uint8_t* src = kp + (ok ? (j * 8 + g) * (D * S::KB) + c * 16 : 0);
-#pragma unroll
-          for (int x = 0; x < S::KC; ++x)
-            copy_async<16>(dst + (j * S::KC + x) * 512 + lane * 16, src + (ok ? x * 64 : 0), ok);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = 2 * c + (j & 1) + 8 * (j >> 1);
-          const bool ok = good && t < left;
-          const uint8_t* src = vp + (ok ? t * (D * S::VB) + g * S::VW : 0);
-#pragma unroll
-          for (int x = 0; x < S::VC; ++x)
-            copy_async<S::VW>(dst + S::K_BYTES + (j * S::VC + x) * (S::VW * 32) + lane * S::VW,
-                              src + (ok ? x * 8 * S::VW : 0), ok);
-        }
-        if (S::KS) {
-          // lanes 0..15: K's scales, 16..31: V's
-          const int t = lane & 15;
-          const bool ok = good && t < left;
-          const float* src = lane < 16 || !S::VS ? p.ks + page * p.ks_page + in_page : p.vs + page * p.vs_page + in_page;
-          if (lane < 16 || S::VS)
-            copy_async<4>(dst + S::K_BYTES + S::V_BYTES + lane * 4, src + (ok ? t : 0), ok);
+        const bool in = iss.step * S::TOK + 16 * s < iss.len;
+        const int page = in ? next_page() : -1;
+        const bool good = page >= 0 && page < p.num_pages;
+        if (!good) gone |= 1u << s;
+        if (lane == 0) {
+          // the last tile's arrival closes the stage's count
+          const uint32_t n = good ? 16 * S::TOKEN : 0;
+          if (s + 1 < S::SUB) mbar_expect_tx(bar + slot, n);
+          else mbar_arrive_expect_tx(bar + slot, n);
+          if (good) copy(stage, bar + slot, page, 16 * s, 16);
         }
         tile_off += 16;
-        if (tile_off >= p.page_size) {
+        if (tile_off == p.page_size) {
           tile_off = 0;
           ++tile_page;
         }
       }
-      if (lane == 0)
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + S::SUB * S::TILE), "r"(bad) : "memory");
-      --iss_left;
-      if (++iss.step == iss.steps && iss_left > 0) {  // on to the next segment
-        iss.step = 0;
-        if (++iss.z == HZ) {
-          iss.z = 0;
-          do {
-            ++iss.b;
-            iss.steps = s_prefix[iss.b + 1] - s_prefix[iss.b];
-          } while (iss.steps == 0);
-          iss.len = clamp_len(p, p.lens[iss.b]);
-        }
-        seek();
-      }
     }
-    copy_commit();
+    absent = (absent & ~(15u << 4 * slot)) | gone << 4 * slot;
+    --iss_left;
+    if (++iss.step == iss.steps && iss_left > 0) {  // on to the next segment
+      iss.step = 0;
+      if (++iss.z == HZ) {
+        iss.z = 0;
+        do {
+          ++iss.b;
+          iss.steps = s_prefix[iss.b + 1] - s_prefix[iss.b];
+        } while (iss.steps == 0);
+        iss.len = clamp_len(p, p.lens[iss.b]);
+      }
+      seek();
+    }
   };
 
 #pragma unroll
@@ -412,6 +398,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
 
   // ---- consume side
   int slot = 0;
+  uint32_t parity = 0;
   int64_t left = end - at;
   bool first_piece = true;
   do {
@@ -468,35 +455,71 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
     }
 
     for (; cur.step < stop; ++cur.step, --left) {
-      copy_wait<kStages - 2>();
-      __syncwarp();
+      __syncwarp();  // every lane is done with the stage that is filled next
       {
         int next = slot + kStages - 1;
         if (next >= kStages) next -= kStages;
         issue(next);
       }
-      const uint32_t base = ring + slot * S::STAGE;
-      if (++slot == kStages) slot = 0;
+      uint8_t* const base = ring + slot * S::STAGE;
+      const bool there = mbar_wait(bar + slot, parity, s_abort + warp, p.timeout_ns, 0xD0);
+      if (!__all_sync(0xffffffffu, there)) {
+        // Given up (the error word says so).  The copies under way write to this
+        // CTA's memory: wait for them too, as long again at most.
+        const uint64_t since = globaltimer();
+        for (int64_t n = left; n > 0 && n > left - kStages; --n) {
+          while (!mbar_try_wait_hint(bar + slot, parity) && globaltimer() - since < p.timeout_ns) {
+          }
+          if (++slot == kStages) {
+            slot = 0;
+            parity ^= 1;
+          }
+        }
+        return;
+      }
+      const int t0 = cur.step * S::TOK;
+      const uint32_t gone = absent >> 4 * slot & 15;
+      if (++slot == kStages) {
+        slot = 0;
+        parity ^= 1;
+      }
+      // Behind the last token the page may hold anything, and a tile on no page
+      // was not copied.  Their scores are masked below; their V is zeroed here,
+      // since 0 * NaN would reach the sums.
+      if (t0 + S::TOK > cur.len || gone != 0) {
+#pragma unroll
+        for (int u = 0; u < S::SUB; ++u) {
+          const int have = gone >> u & 1 ? 0 : min(16, max(0, cur.len - t0 - 16 * u));
+          for (int i = 16 * (have * (S::VROW / 16) + lane); i < 16 * S::VROW; i += 512)
+            *reinterpret_cast<uint4*>(base + S::V_AT + 16 * u * S::VROW + i) = make_uint4(0, 0, 0, 0);
+          if (S::VS && lane >= have && lane < 16)
+            *reinterpret_cast<float*>(base + S::VS_AT + (16 * u + lane) * 4) = 0.f;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      }
 
       // ---- scores, in units of log2
       float s[NT][S::SUB][4];
 #pragma unroll
       for (int u = 0; u < S::SUB; ++u) {
-        const uint32_t kb = base + u * S::TILE + lane * 16;
+        const uint8_t* const kb = base + (16 * u + g) * S::KROW + c * 16;
+        float s2[NT][4];  // a second accumulator: two chains of products, half as long
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][u][e] = 0.f;
+          for (int e = 0; e < 4; ++e) s[n][u][e] = s2[n][e] = 0.f;
 #pragma unroll
         for (int x = 0; x < S::KC; ++x) {
-          const uint4 w0 = lds128(kb + x * 512), w1 = lds128(kb + (S::KC + x) * 512);
+          const uint4 w0 = *reinterpret_cast<const uint4*>(kb + x * 64);
+          const uint4 w1 = *reinterpret_cast<const uint4*>(kb + 8 * S::KROW + x * 64);
           const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w};
           if (S::KB == 2) {
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               const uint32_t a[4] = {a0[2 * y], a1[2 * y], a0[2 * y + 1], a1[2 * y + 1]};
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816<T>(s[n][u], a, qf[n][2 * x + y][0], qf[n][2 * x + y][1]);
+              for (int n = 0; n < NT; ++n) mma16816<T>(y ? s2[n] : s[n][u], a, qf[n][2 * x + y][0], qf[n][2 * x + y][1]);
             }
           } else {
 #pragma unroll
@@ -506,28 +529,27 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
               codes_to_16<T>(a1[y], a[1], a[3]);
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                mma16816<T>(s[n][u], a, qf[n][(4 * x + y) % (D / 16)][0], qf[n][(4 * x + y) % (D / 16)][1]);
+                mma16816<T>(y & 1 ? s2[n] : s[n][u], a, qf[n][(4 * x + y) % (D / 16)][0],
+                            qf[n][(4 * x + y) % (D / 16)][1]);
             }
           }
         }
         float f0 = p.scale_log2, f1 = p.scale_log2;
         if (S::KS) {
-          const uint32_t sb = base + u * S::TILE + S::K_BYTES + S::V_BYTES;
-          f0 *= lds32(sb + g * 4);
-          f1 *= lds32(sb + (g + 8) * 4);
+          const uint8_t* const sb = base + S::KS_AT + u * 64;
+          f0 *= *reinterpret_cast<const float*>(sb + g * 4);
+          f1 *= *reinterpret_cast<const float*>(sb + (g + 8) * 4);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          s[n][u][0] *= f0;
-          s[n][u][1] *= f0;
-          s[n][u][2] *= f1;
-          s[n][u][3] *= f1;
+          s[n][u][0] = (s[n][u][0] + s2[n][0]) * f0;
+          s[n][u][1] = (s[n][u][1] + s2[n][1]) * f0;
+          s[n][u][2] = (s[n][u][2] + s2[n][2]) * f1;
+          s[n][u][3] = (s[n][u][3] + s2[n][3]) * f1;
         }
       }
       // ---- masks: the end of the cache, later query tokens' keys, bad pages
-      const uint32_t bad = __float_as_uint(lds32(base + S::SUB * S::TILE));
-      const int t0 = cur.step * S::TOK;
-      if (t0 + S::TOK > vis_min || bad != 0) {
+      if (t0 + S::TOK > vis_min || gone != 0) {
 #pragma unroll
         for (int u = 0; u < S::SUB; ++u)
 #pragma unroll
@@ -535,7 +557,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int t = t0 + 16 * u + g + 8 * (e >> 1);
-              if (t >= vis[n][e & 1] || (bad >> u & 1)) s[n][u][e] = -INFINITY;
+              if (t >= vis[n][e & 1] || (gone >> u & 1)) s[n][u][e] = -INFINITY;
             }
       }
       // ---- running maxima: reduced over the lanes only when one grew
@@ -578,16 +600,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
       // ---- probabilities and O^T += V^T P^T
 #pragma unroll
       for (int u = 0; u < S::SUB; ++u) {
-        const uint32_t vb = base + u * S::TILE + S::K_BYTES + lane * S::VW;
+        const uint8_t* const vb = base + S::V_AT + (16 * u + 2 * c) * S::VROW + g * S::VW;
         uint32_t pf[NT][2];
         float f0 = 1.f, f1 = 1.f;
         if (S::VS) {
           // fp16: times 448, i.e. the row's largest |v|, which fp16 can hold;
           // delta_V itself would push small rows into fp16's subnormals
           const float up = std::is_same<T, __half>::value ? 448.f : 1.f;
-          const uint32_t sb = base + u * S::TILE + S::K_BYTES + S::V_BYTES + 64;
-          f0 = lds32(sb + g * 4) * up;
-          f1 = lds32(sb + (g + 8) * 4) * up;
+          const uint8_t* const sb = base + S::VS_AT + u * 64;
+          f0 = *reinterpret_cast<const float*>(sb + g * 4) * up;
+          f1 = *reinterpret_cast<const float*>(sb + (g + 8) * 4) * up;
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -608,8 +630,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
 #pragma unroll
         for (int x = 0; x < S::VC; ++x) {
           if (S::VB == 2) {
-            const uint4 r0 = lds128(vb + x * 512), r1 = lds128(vb + (S::VC + x) * 512);
-            const uint4 r2 = lds128(vb + (2 * S::VC + x) * 512), r3 = lds128(vb + (3 * S::VC + x) * 512);
+            const uint8_t* const v0 = vb + x * 128;
+            const uint4 r0 = *reinterpret_cast<const uint4*>(v0);
+            const uint4 r1 = *reinterpret_cast<const uint4*>(v0 + S::VROW);
+            const uint4 r2 = *reinterpret_cast<const uint4*>(v0 + 8 * S::VROW);
+            const uint4 r3 = *reinterpret_cast<const uint4*>(v0 + 9 * S::VROW);
             const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
             const uint32_t w2[4] = {r2.x, r2.y, r2.z, r2.w}, w3[4] = {r3.x, r3.y, r3.z, r3.w};
 #pragma unroll
@@ -623,14 +648,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
             uint32_t w[4][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+              const uint8_t* const v0 = vb + ((j & 1) + 8 * (j >> 1)) * S::VROW;
               if (S::VW == 16) {
-                const uint4 r = lds128(vb + j * 512);
+                const uint4 r = *reinterpret_cast<const uint4*>(v0);
                 w[j][0] = r.x;
                 w[j][1] = r.y;
                 w[j][2] = r.z;
                 w[j][3] = r.w;
               } else {
-                const uint2 r = lds64(vb + j * 256);
+                const uint2 r = *reinterpret_cast<const uint2*>(v0);
                 w[j][0] = r.x;
                 w[j][1] = r.y;
               }
@@ -886,6 +912,15 @@ cudaError_t launch_d(const DecodeParams& p, const Plan& P, int format, cudaStrea
 
 }  // namespace
 
+cudaError_t decode_read_and_clear_error(uint32_t* word) {
+  uint32_t w = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&w, g_error_word, sizeof(w));
+  if (e != cudaSuccess) return e;
+  if (w != 0) e = cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero));
+  *word = w;
+  return e;
+}
+
 size_t decode_workspace_bytes(int B, int H, int H_kv, int n_q, int d, int max_len, int format) {
   return plan_of(B, H, H_kv, n_q, d, max_len, format).bytes;
 }
@@ -927,6 +962,7 @@ cudaError_t launch_attn_decode(const DecodeArgs& a, cudaStream_t st) {
   p.max_len = c.num_pages > 0 ? a.max_len : 0;  // no page: no token
   p.causal = a.causal;
   p.workers = P.workers;
+  p.timeout_ns = a.timeout_ns;
   p.scale_log2 = a.sm_scale * 1.4426950408889634f;
   if (c.dtype == SAGE_F16)
     return c.d == 64 ? launch_d<__half, 64>(p, P, c.format, st) : launch_d<__half, 128>(p, P, c.format, st);

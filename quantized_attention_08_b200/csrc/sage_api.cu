@@ -201,7 +201,8 @@ sage_status_t check_cache(const sage_kv_cache_t* c) {
   if (c->k_page_stride < rows * c->d || c->v_page_stride < rows * c->d ||
       (ks && c->k_scale_page_stride < rows) || (vs && c->v_scale_page_stride < rows))
     return SAGE_ERR_INVALID_ARG;
-  if (!a16(c->k) || !a16(c->v) || (ks && !a4(c->k_scale)) || (vs && !a4(c->v_scale)) ||
+  if (!a16(c->k) || !a16(c->v) || (ks && !a16(c->k_scale)) || (vs && !a16(c->v_scale)) ||
+      (ks && c->k_scale_page_stride % 4 != 0) || (vs && c->v_scale_page_stride % 4 != 0) ||
       c->k_page_stride % (ks ? 16 : 8) != 0 || c->v_page_stride % (vs ? 16 : 8) != 0)
     return SAGE_ERR_MISALIGNED;
   return SAGE_OK;
@@ -961,6 +962,7 @@ sage_status_t sage_attn_decode_paged(const void* q, const int64_t* q_strides,
   a.max_len = max_len;
   a.causal = causal;
   a.sm_scale = sm_scale;
+  a.timeout_ns = g_timeout_ns.load();
   if ((s = check_device()) != SAGE_OK) return s;
   return from_cuda(sage::launch_attn_decode(a, static_cast<cudaStream_t>(stream)));
 }
@@ -969,8 +971,10 @@ int sage_v_hat_layout(void) { return 0; }
 
 sage_status_t sage_get_device_error(void* stream, uint32_t* detail) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return SAGE_ERR_CUDA;
-  uint32_t w = 0;
+  uint32_t w = 0, wd = 0;
   if (sage::read_and_clear_error(&w) != cudaSuccess) return SAGE_ERR_CUDA;
+  if (sage::decode_read_and_clear_error(&wd) != cudaSuccess) return SAGE_ERR_CUDA;
+  w |= wd;
   if (detail) *detail = w;
   return (w & sage::ERR_TIMEOUT) ? SAGE_ERR_DEVICE_TIMEOUT : SAGE_OK;
 }

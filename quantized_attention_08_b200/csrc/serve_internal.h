@@ -65,8 +65,10 @@ struct DecodeArgs {
   void* ws;
   int max_pages, B, H, n_q, max_len, causal;
   float sm_scale;
+  uint64_t timeout_ns;   // of the kernel's waits
 };
 size_t decode_workspace_bytes(int B, int H, int H_kv, int n_q, int d, int max_len, int format);
+cudaError_t decode_read_and_clear_error(uint32_t* word);
 cudaError_t launch_attn_decode(const DecodeArgs& a, cudaStream_t st);
 
 }  // namespace sage

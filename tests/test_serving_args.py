@@ -32,7 +32,7 @@ BAD_CACHES = [(dict(k=None), 1), (dict(v=None), 1), (dict(k_scale=None), 1), (di
               (dict(num_pages=-1), 1), (dict(page_size=0), 1), (dict(H_kv=0), 1), (dict(k_page_stride=16384 - 16), 1),
               (dict(v_scale_page_stride=127), 1), (dict(d=96), 2), (dict(page_size=40), 2), (dict(format=3), 2),
               (dict(dtype=2), 2), (dict(num_pages=1 << 26), 2), (dict(k=OK + 4), 3), (dict(v_scale=OK + 2), 3),
-              (dict(v_page_stride=16384 + 8), 3)]
+              (dict(v_page_stride=16384 + 8), 3), (dict(k_scale=OK + 8), 3), (dict(k_scale_page_stride=130), 3)]
 
 
 def strides(*s):
