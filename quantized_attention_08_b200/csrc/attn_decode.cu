@@ -5,22 +5,26 @@
 //   m = max s, l = sum exp(s_t - m), o = sum exp(s_t - m) v_t / l
 //
 // Bound by HBM: each visible key and value is read once and serves all G
-// query heads of its group (and all query tokens).
+// query heads of its group (and all query tokens).  Measured on one B200,
+// device time with the join: 90 us for one request of 131072 tokens (H 32,
+// H_kv 8, d 128, bf16: 537 MB, 0.91 of the measured copy rate), 96 us for 64
+// requests of 1 to 8192 tokens in 8+8 (570 MB, 0.90).
 //
 // Work.  The cache of one (request, kv head, group of query rows) is a
-// segment of steps of kStep tokens.  All segments' steps stand in one line,
-// and every warp of the grid takes an equal stretch of it, whatever the
-// lengths: a long request is split over many warps, short ones share one.
+// segment of steps of S::TOK tokens.  All segments' steps stand in one line,
+// and every consuming warp of the grid takes an equal stretch of it, whatever
+// the lengths: a long request is split over many warps, short ones share one.
 // The lengths stay on the device; each CTA forms their prefix sum.  A segment
 // inside one warp's stretch is finished there; the pieces of the others go to
 // the workspace as (m, l, o) and a second kernel joins them in a fixed order.
 //
-// Loads.  One lane of a warp feeds the warp's own ring in shared memory with
-// bulk copies of whole rows (a step of a page is one run of memory for each of
-// K, V and the scales), counted by an mbarrier a stage; no other warp is
-// involved.  cp.async by the lanes that later read the bytes, in fragment order,
-// reached 4.9 TB/s where rows in order reach 6.5 (eight lanes then touch two
-// to four lines at once).
+// Loads.  Loading warps feed a ring in shared memory for each consuming warp
+// with bulk copies of whole rows (a step of a page is one run of memory for
+// each of K, V and the scales), counted by an mbarrier a stage.  cp.async by the
+// lanes that later read the bytes, in fragment order, reached 4.9 TB/s where
+// rows in order reach 6.5 (eight lanes then touch two to four lines at once);
+// copies issued by the consuming warps themselves cost those a third of their
+// instructions.  A stage is released once K is multiplied and V is in registers.
 //
 // Products.  mma.sync m16n8k16, transposed: S^T = K q^T and O^T = V^T P^T,
 // with tokens (channels) on the 16 side and query rows on the 8 side, since
@@ -29,10 +33,11 @@
 // rows the tensor work here is a few percent of what HBM leaves time for.
 // The order of k inside the products is free, so a lane's 16-byte pieces of
 // K's rows serve as fragments as they are; pairs of V's rows are interleaved
-// with prmt.  int8 codes become 16-bit numbers exactly; delta_K multiplies the
-// fp32 scores, delta_V the probabilities.  S, m, l, O are fp32; P is rounded
-// to 16 bits for its product (2^-12 or 2^-9 relative, as every 16-bit
-// attention does), l sums the unrounded values.
+// with prmt.  int8 and E4M3 codes become fp16 numbers exactly; delta_K multiplies
+// the fp32 scores, delta_V enters the exponents of the probabilities that
+// multiply V, which are then at most 1 whatever V's range.  S, m, l, O are fp32;
+// P is rounded to 16 bits for its product (2^-12 or 2^-9 relative, as every
+// 16-bit attention does), l sums the unrounded values.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -49,9 +54,13 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kStages = 3;
+constexpr int kFeeders = 4;   // loading warps
 constexpr int kMaxBatch = 4096;   // prefix sums in shared memory
 constexpr int kSms = 148;
 constexpr int kMinSteps = 2;      // of one warp's stretch
+// What beginning a segment costs, in steps: the line counts each segment as that
+// much longer, so that a warp with many short ones gets fewer steps.
+constexpr int kSegmentCost = 2;
 
 struct DecodeParams {
   const uint8_t* q;
@@ -68,10 +77,9 @@ struct DecodeParams {
   float* lse;
   float* part_o;                 // [2 * workers][rows of a group][D]
   float2* part_ml;               // [2 * workers][rows of a group]
-  int* prefix;                   // [B + 1] steps before each request
   int num_pages, page_size, max_pages;
   int B, H, Hk, G, n_q, rows, groups;  // rows = G * n_q in `groups` groups of 8 NT
-  int max_len, causal, workers;
+  int max_len, causal, workers, step_tokens;
   float scale_log2;
   uint64_t timeout_ns;
 };
@@ -111,43 +119,30 @@ __device__ __forceinline__ uint32_t bytes(uint32_t a, uint32_t b, uint32_t sel) 
   return __byte_perm(a, b, sel);
 }
 
-// Four int8 codes as four 16-bit numbers, exactly.
-//  fp16: 1024 + (code + 128) is the bit pattern 0x64 followed by the biased
-//        byte; subtracting 1152 leaves the code.
-//  bf16: 128 + (low seven bits) is 0x43 followed by them, and 0x43 followed by
-//        the top bit alone is 128 or 256; the difference is the code.
 template <typename T>
-__device__ __forceinline__ void codes_to_16(uint32_t w, uint32_t& lo, uint32_t& hi);
+__device__ __forceinline__ float2 unpack16(uint32_t w);
 template <>
-__device__ __forceinline__ void codes_to_16<__half>(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
-  uint32_t x = bytes(u, 0x64646464u, 0x4140), y = bytes(u, 0x64646464u, 0x4342);
-  const __half2 a = __hsub2(*reinterpret_cast<__half2*>(&x), bias);
-  const __half2 b = __hsub2(*reinterpret_cast<__half2*>(&y), bias);
-  lo = *reinterpret_cast<const uint32_t*>(&a);
-  hi = *reinterpret_cast<const uint32_t*>(&b);
+__device__ __forceinline__ float2 unpack16<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 template <>
-__device__ __forceinline__ void codes_to_16<__nv_bfloat16>(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t m = w & 0x7f7f7f7fu, s = w & 0x80808080u;
-  uint32_t x0 = bytes(m, 0x43434343u, 0x4140), x1 = bytes(m, 0x43434343u, 0x4342);
-  uint32_t y0 = bytes(s, 0x43434343u, 0x4140), y1 = bytes(s, 0x43434343u, 0x4342);
-  const __nv_bfloat162 a = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x0), *reinterpret_cast<__nv_bfloat162*>(&y0));
-  const __nv_bfloat162 b = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x1), *reinterpret_cast<__nv_bfloat162*>(&y1));
-  lo = *reinterpret_cast<const uint32_t*>(&a);
-  hi = *reinterpret_cast<const uint32_t*>(&b);
+__device__ __forceinline__ float2 unpack16<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// Four int8 codes as four fp16 numbers: code + 128 (0 .. 255) taken as fp16 bits
+// is a subnormal, (code + 128) 2^-24 exactly, which the MMA multiplies as any
+// other number; three instructions where a conversion takes five (and eight to
+// bf16).
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  lo = bytes(u, 0, 0x4140);
+  hi = bytes(u, 0, 0x4342);
 }
 
 // Four E4M3 codes of token t (word a) and of token t' (word b), as four pairs
-// (t, t') of 16-bit numbers, exactly.
-//  bf16: E4M3's exponent and mantissa bits, moved to the low end of bf16's
-//        exponent and the top of its mantissa, read 2^-120 times the number
-//        (its subnormals too).
-template <typename T>
-__device__ __forceinline__ void e4m3_pairs(uint32_t a, uint32_t b, uint32_t* out);
-template <>
-__device__ __forceinline__ void e4m3_pairs<__half>(uint32_t a, uint32_t b, uint32_t* out) {
+// (t, t') of fp16 numbers, exactly.
+__device__ __forceinline__ void e4m3_pairs(uint32_t a, uint32_t b, uint32_t* out) {
   const uint32_t x = bytes(a, b, 0x5140), y = bytes(a, b, 0x7362);
   asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;}"
       : "=r"(out[0]), "=r"(out[1])
@@ -155,17 +150,6 @@ __device__ __forceinline__ void e4m3_pairs<__half>(uint32_t a, uint32_t b, uint3
   asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;}"
       : "=r"(out[2]), "=r"(out[3])
       : "r"(y));
-}
-template <>
-__device__ __forceinline__ void e4m3_pairs<__nv_bfloat16>(uint32_t a, uint32_t b, uint32_t* out) {
-  const __nv_bfloat162 up = __bfloat162bfloat162(__ushort_as_bfloat16(0x7b80));  // 2^120
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t y = bytes(a, b, 0x4400 + 0x1111 * i);
-    uint32_t z = (y & 0x80008000u) | ((y >> 4) & 0x07f007f0u);
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&z), up);
-    out[i] = *reinterpret_cast<const uint32_t*>(&r);
-  }
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -177,6 +161,28 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// maximum over the lanes that hold the same two rows of S^T (other tokens)
+__device__ __forceinline__ float token_max(float v) {
+#pragma unroll
+  for (int o = 4; o <= 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
 }
 
 // Bulk copy of n bytes (a multiple of 16; both addresses 16-byte aligned),
@@ -211,6 +217,13 @@ struct Step {
 };
 
 inline __host__ __device__ int steps_of(int len, int tok) { return (len + tok - 1) / tok; }
+// places of a segment in the line
+inline __host__ __device__ int places_of(int len, int tok) { return len > 0 ? steps_of(len, tok) + kSegmentCost : 0; }
+// places of a worker
+inline __host__ __device__ int64_t per_worker(int64_t total, int workers) {
+  const int64_t per = (total + workers - 1) / workers;
+  return per > kMinSteps ? per : kMinSteps;
+}
 
 __device__ __forceinline__ int clamp_len(const DecodeParams& p, int len) {
   const int64_t room = static_cast<int64_t>(p.max_pages) * p.page_size;
@@ -225,38 +238,232 @@ struct Cursor {
 };
 
 // ------------------------------------------------------------- the kernel
+// A worker's part of the line: where it begins, and how many of its places are
+// left, counted from the first that holds a step.  A segment takes kSegmentCost
+// places without a step, then one for each of its steps.
+struct Stretch {
+  Cursor cur;
+  int64_t left;
+};
+
+template <typename S, bool SPLIT>
+__device__ __forceinline__ Stretch stretch_of(const DecodeParams& p, const int* s_prefix, int worker) {
+  Stretch w;
+  const int HZ = p.Hk * p.groups;
+  if (SPLIT) {
+    const int64_t total = static_cast<int64_t>(s_prefix[p.B]) * HZ;
+    const int64_t per = per_worker(total, p.workers);
+    int64_t at = worker * per;
+    const int64_t end = worker < p.workers ? min(total, at + per) : 0;
+    w.left = 0;
+    if (at >= end) return w;
+    // the request that holds place `at`: the last one with prefix * HZ <= at
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (static_cast<int64_t>(s_prefix[mid]) * HZ <= at) lo = mid; else hi = mid;
+    }
+    const int places = s_prefix[lo + 1] - s_prefix[lo];
+    const int64_t in = at - static_cast<int64_t>(s_prefix[lo]) * HZ;
+    w.cur.b = lo;
+    w.cur.steps = places - kSegmentCost;
+    w.cur.z = static_cast<int>(in / places);
+    const int place = static_cast<int>(in - static_cast<int64_t>(w.cur.z) * places);
+    w.cur.step = max(0, place - kSegmentCost);
+    w.cur.len = clamp_len(p, p.lens[lo]);
+    // places at the segment's beginning that hold no step
+    w.left = end - at - max(0, kSegmentCost - place);
+  } else {  // a segment a worker
+    w.left = 0;
+    w.cur.b = -1;
+    if (worker >= p.B * HZ) return w;
+    w.cur.b = worker / HZ;
+    w.cur.z = worker - w.cur.b * HZ;
+    w.cur.step = 0;
+    w.cur.len = clamp_len(p, p.lens[w.cur.b]);
+    w.cur.steps = steps_of(w.cur.len, S::TOK);
+    w.left = w.cur.steps;
+  }
+  return w;
+}
+
+// On to the next segment that has steps (the caller knows that places are left
+// beyond this one); those it has without a step are taken off `left`.
+__device__ __forceinline__ void next_segment(const DecodeParams& p, const int* s_prefix, Cursor& c, int64_t& left) {
+  left -= kSegmentCost;
+  c.step = 0;
+  if (++c.z < p.Hk * p.groups) return;
+  c.z = 0;
+  do {
+    ++c.b;
+    c.steps = s_prefix[c.b + 1] - s_prefix[c.b] - kSegmentCost;
+  } while (c.steps <= 0);
+  c.len = clamp_len(p, p.lens[c.b]);
+}
+
+// The loading warp: lane w feeds the ring of warp w, so that one instruction
+// stream serves all of them.  The page numbers of a lane's next step are read
+// while the current one is copied.
+template <typename S, bool SPLIT>
+__device__ __forceinline__ void feed(const DecodeParams& p, const int* s_prefix, uint8_t* smem, uint64_t* full,
+                                     uint64_t* empty, uint32_t* absent, volatile int* abort_flag, int feeder,
+                                     int lane) {
+  Stretch w;
+  w.left = 0;
+  // A bulk copy takes its warp about 120 cycles, whichever lane it is for, and a
+  // step has to be begun every 350 cycles of an SM to keep HBM busy: with two
+  // copies a step one warp does for all (and in a fairer order: 90 us where four
+  // take 95, 131072 tokens of 16 bits), with more all four share them (97 us
+  // where one takes 125, 64 requests of 8+8).
+  const bool one_page = p.page_size % S::TOK == 0;  // a step lies in one page
+  const int feeders = (one_page ? 1 : S::SUB) * (2 + S::KS + S::VS) <= 2 ? 1 : kFeeders;
+  const int of = feeder < feeders ? feeder + lane * feeders : kWarps;  // the warp that this lane feeds
+  if (of < kWarps) w = stretch_of<S, SPLIT>(p, s_prefix, of * gridDim.x + blockIdx.x);
+  int64_t left = w.left;
+  int issued = 0;  // stages filled, kStages at most
+  uint8_t* const ring = smem + of * (kStages * S::STAGE);
+  full += of * kStages;
+  empty += of * kStages;
+  absent += of * kStages;
+  Cursor& c = w.cur;
+  int tile_page = 0, tile_off = 0;                  // page index and offset of the next step
+  int ids[S::SUB];                                  // its pages, one a tile (or one)
+  auto fetch = [&]() {
+#pragma unroll
+    for (int s = 0; s < S::SUB; ++s) {
+      if (s > 0 && one_page) break;
+      int pg = tile_page, off = tile_off + 16 * s;
+      while (off >= p.page_size) {
+        off -= p.page_size;
+        ++pg;
+      }
+      const bool in = c.step * S::TOK + 16 * s < c.len;
+      ids[s] = in ? p.table[static_cast<int64_t>(c.b) * p.max_pages + pg] : -1;
+    }
+  };
+  auto seek = [&]() {
+    const int t = c.step * S::TOK;
+    tile_page = t / p.page_size;
+    tile_off = t - tile_page * p.page_size;
+  };
+  if (left > 0) {
+    seek();
+    fetch();
+  }
+  int slot = 0;
+  uint32_t parity = 0, round = 0;
+  uint64_t since = 0;
+  while (__any_sync(0xffffffffu, left > 0)) {
+    bool moved = false;
+    if (left > 0 && (round == 0 || mbar_test_wait(empty + slot, parity ^ 1))) {
+      moved = true;
+      const int64_t head = static_cast<int64_t>(c.z / p.groups) * p.page_size;
+      const uint32_t dst = smem_u32(ring + slot * S::STAGE);
+      uint64_t* const bar = full + slot;
+      uint32_t gone = 0, bytes = 0;
+      const int tiles = one_page ? 1 : S::SUB;
+      const int n = one_page ? S::TOK : 16;
+#pragma unroll
+      for (int s = 0; s < S::SUB; ++s) {
+        if (s >= tiles) break;
+        if (static_cast<uint32_t>(ids[s]) < static_cast<uint32_t>(p.num_pages)) bytes += n * S::TOKEN;
+        else gone |= (one_page ? (1u << S::SUB) - 1 : 1u << s);
+      }
+      absent[slot] = gone;
+      mbar_arrive_expect_tx(bar, bytes);
+      int off = tile_off;
+#pragma unroll
+      for (int s = 0; s < S::SUB; ++s) {
+        if (s >= tiles) break;
+        const int64_t page = ids[s], row = head + off;
+        if (static_cast<uint32_t>(ids[s]) < static_cast<uint32_t>(p.num_pages)) {
+          const int at = 16 * s;
+          bulk_load(dst + at * S::KROW, p.k + page * p.k_page + row * S::KROW, n * S::KROW, bar);
+          bulk_load(dst + S::V_AT + at * S::VROW, p.v + page * p.v_page + row * S::VROW, n * S::VROW, bar);
+          if (S::KS) bulk_load(dst + S::KS_AT + at * 4, p.ks + page * p.ks_page + row, n * 4, bar);
+          if (S::VS) bulk_load(dst + S::VS_AT + at * 4, p.vs + page * p.vs_page + row, n * 4, bar);
+        }
+        off += 16;
+        if (off >= p.page_size) off = 0;
+      }
+      --left;
+      if (issued < kStages) ++issued;
+      if (left > 0) {
+        tile_off += S::TOK;
+        while (tile_off >= p.page_size) {
+          tile_off -= p.page_size;
+          ++tile_page;
+        }
+        if (++c.step == c.steps) {
+          next_segment(p, s_prefix, c, left);
+          seek();
+        }
+        if (left > 0) fetch();
+      }
+      if (++slot == kStages) {
+        slot = 0;
+        ++round;
+        parity ^= 1;
+      }
+    }
+    if (__any_sync(0xffffffffu, moved)) {
+      since = 0;
+    } else {  // every ring is full: nothing to do for a while
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+      const uint64_t now = globaltimer();
+      if (since == 0) since = now;
+      if (__any_sync(0xffffffffu, now - since > p.timeout_ns)) {
+        if (lane == 0) atomicOr(&g_error_word, ERR_TIMEOUT | (0xD1u << 8));
+        *abort_flag = 1;
+        break;
+      }
+      __nanosleep(20);
+    }
+  }
+  if (__any_sync(0xffffffffu, *abort_flag != 0)) {
+    // Given up.  The copies under way write to this CTA's memory: wait for
+    // them, as long again at most.
+    since = globaltimer();
+    while (issued-- > 0) {
+      if (--slot < 0) {
+        slot = kStages - 1;
+        parity ^= 1;
+      }
+      while (!mbar_test_wait(full + slot, parity) && globaltimer() - since < p.timeout_ns) {
+      }
+    }
+  }
+}
+
 template <typename T, int D, int FMT, int NT, bool SPLIT>
-__global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodeParams p) {
+__global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(const DecodeParams p) {
   using S = Step<D, FMT>;
+  // int8 K and E4M3 V become fp16 whatever the model's type is
+  using TK = typename std::conditional<FMT == SAGE_KV_16, T, __half>::type;
+  using TV = typename std::conditional<FMT == SAGE_KV_8P8, __half, T>::type;
   constexpr int ROWS = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_scan[kWarps];
+  __shared__ __align__(8) uint64_t s_full[kWarps * kStages], s_empty[kWarps * kStages];
+  __shared__ uint32_t s_absent[kWarps * kStages];  // tiles of a stage that are on no page
+  __shared__ int s_scan[kWarps + kFeeders];
+  __shared__ int s_abort;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  const int HZ = p.Hk * p.groups;
-  uint8_t* const ring = smem + warp * (kStages * S::STAGE);
-  __shared__ __align__(8) uint64_t s_bar[kWarps][kStages];
-  __shared__ int s_abort[kWarps];
-  uint64_t* const bar = s_bar[warp];
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) mbar_init(bar + i, 1);
-    s_abort[warp] = 0;
-    fence_mbar_init();
-  }
-  __syncwarp();
   int* s_prefix = reinterpret_cast<int*>(smem + kWarps * kStages * S::STAGE);  // SPLIT only: [B + 1]
 
-  // ---- this warp's stretch [at, end) of the line
-  // warp-major numbers: few workers then stand on as many SMs as they can
-  const int worker = warp * gridDim.x + blockIdx.x;
-  int64_t at = 0, end = 0;
-  Cursor cur;
+  if (threadIdx.x < kWarps * kStages) {
+    mbar_init(s_full + threadIdx.x, 1);
+    mbar_init(s_empty + threadIdx.x, 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) s_abort = 0;
   if (SPLIT) {
+    // the join's CTAs may be placed now; they wait for this grid's end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int run = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kWarps * 32) {
+    for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
       const int b = b0 + threadIdx.x;
-      int v = b < p.B ? steps_of(clamp_len(p, p.lens[b]), S::TOK) : 0;
+      int v = b < p.B ? places_of(clamp_len(p, p.lens[b]), S::TOK) : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, v, o);
@@ -266,146 +473,42 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
       if (lane == 31) s_scan[warp] = v;
       __syncthreads();
       int before = run;
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < kWarps + kFeeders; ++w) {
         if (w < warp) before += s_scan[w];
         run += s_scan[w];
       }
       if (b < p.B) s_prefix[b + 1] = before + v;
     }
     if (threadIdx.x == 0) s_prefix[0] = 0;
-    __syncthreads();
-    if (blockIdx.x == 0)
-      for (int b = threadIdx.x; b <= p.B; b += kWarps * 32) p.prefix[b] = s_prefix[b];
-    // the join's CTAs may be placed now; they wait for this grid's end
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t total = static_cast<int64_t>(s_prefix[p.B]) * HZ;
-    const int64_t per = max(static_cast<int64_t>(kMinSteps), (total + p.workers - 1) / p.workers);
-    at = worker * per;
-    end = min(total, at + per);
-    if (worker >= p.workers || at >= end) return;
-    // the request that holds step `at`: the last one with prefix * HZ <= at
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (static_cast<int64_t>(s_prefix[mid]) * HZ <= at) lo = mid; else hi = mid;
-    }
-    cur.b = lo;
-    cur.steps = s_prefix[lo + 1] - s_prefix[lo];
-    const int64_t in = at - static_cast<int64_t>(s_prefix[lo]) * HZ;
-    cur.z = static_cast<int>(in / cur.steps);
-    cur.step = static_cast<int>(in - static_cast<int64_t>(cur.z) * cur.steps);
-    cur.len = clamp_len(p, p.lens[lo]);
-  } else {
-    if (worker >= p.B * HZ) return;
-    cur.b = worker / HZ;
-    cur.z = worker % HZ;
-    cur.step = 0;
-    cur.len = clamp_len(p, p.lens[cur.b]);
-    cur.steps = steps_of(cur.len, S::TOK);
-    end = cur.steps;
+  }
+  __syncthreads();
+  // Two tiles of rows need more registers than 12 warps get at launch: the four
+  // loading warps give theirs up (72 + 2 * 216 = 3 * 168).
+  constexpr bool kShift = NT > 1;
+  if (warp >= kWarps) {
+    if (kShift) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    feed<S, SPLIT>(p, s_prefix, smem, s_full, s_empty, s_absent, &s_abort, warp - kWarps, lane);
+    return;
   }
 
-  // ---- issue side
-  Cursor iss = cur;
-  int64_t iss_left = end - at;         // steps not issued yet
-  int tile_page = 0, tile_off = 0;     // page index and offset in the page of the next tile
-  int page_base = -1, page_ids = 0;    // lane i holds table[page_base + i]
-  auto seek = [&]() {
-    const int t = iss.step * S::TOK;
-    tile_page = t / p.page_size;
-    tile_off = t - tile_page * p.page_size;
-    page_base = -1;
-  };
-  seek();
-
-  uint32_t absent = 0;  // 4 bits a stage: tiles on no page
-  // The page of the next tile; page tables are read 32 entries at a time.
-  auto next_page = [&]() {
-    if (page_base < 0 || tile_page >= page_base + 32) {
-      page_base = tile_page;
-      const int i = page_base + lane;
-      page_ids = i < p.max_pages && static_cast<int64_t>(i) * p.page_size < iss.len
-                     ? p.table[static_cast<int64_t>(iss.b) * p.max_pages + i]
-                     : -1;
-    }
-    return __shfl_sync(0xffffffffu, page_ids, tile_page - page_base);
-  };
-  // Copies of n tokens from offset tile_off of `page` to row `at` of a stage.
-  auto copy = [&](uint8_t* stage, uint64_t* b, int page, int at, int n) {
-    const int64_t in_page = static_cast<int64_t>(iss.z / p.groups) * p.page_size + tile_off;
-    const uint32_t dst = smem_u32(stage);
-    bulk_load(dst + at * S::KROW, p.k + page * p.k_page + in_page * S::KROW, n * S::KROW, b);
-    bulk_load(dst + S::V_AT + at * S::VROW, p.v + page * p.v_page + in_page * S::VROW, n * S::VROW, b);
-    if (S::KS) bulk_load(dst + S::KS_AT + at * 4, p.ks + page * p.ks_page + in_page, n * 4, b);
-    if (S::VS) bulk_load(dst + S::VS_AT + at * 4, p.vs + page * p.vs_page + in_page, n * 4, b);
-  };
-  auto issue = [&](int slot) {
-    if (iss_left <= 0) return;
-    uint8_t* const stage = ring + slot * S::STAGE;
-    uint32_t gone = 0;
-    if (p.page_size % S::TOK == 0) {  // a step lies in one page
-      const int page = next_page();
-      const bool good = page >= 0 && page < p.num_pages;
-      if (!good) gone = (1u << S::SUB) - 1;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar + slot, good ? S::TOK * S::TOKEN : 0);
-        if (good) copy(stage, bar + slot, page, 0, S::TOK);
-      }
-      tile_off += S::TOK;
-      if (tile_off == p.page_size) {
-        tile_off = 0;
-        ++tile_page;
-      }
-    } else {
-#pragma unroll
-      for (int s = 0; s < S::SUB; ++s) {
-        const bool in = iss.step * S::TOK + 16 * s < iss.len;
-        const int page = in ? next_page() : -1;
-        const bool good = page >= 0 && page < p.num_pages;
-        if (!good) gone |= 1u << s;
-        if (lane == 0) {
-          // the last tile's arrival closes the stage's count
-          const uint32_t n = good ? 16 * S::TOKEN : 0;
-          if (s + 1 < S::SUB) mbar_expect_tx(bar + slot, n);
-          else mbar_arrive_expect_tx(bar + slot, n);
-          if (good) copy(stage, bar + slot, page, 16 * s, 16);
-        }
-        tile_off += 16;
-        if (tile_off == p.page_size) {
-          tile_off = 0;
-          ++tile_page;
-        }
-      }
-    }
-    absent = (absent & ~(15u << 4 * slot)) | gone << 4 * slot;
-    --iss_left;
-    if (++iss.step == iss.steps && iss_left > 0) {  // on to the next segment
-      iss.step = 0;
-      if (++iss.z == HZ) {
-        iss.z = 0;
-        do {
-          ++iss.b;
-          iss.steps = s_prefix[iss.b + 1] - s_prefix[iss.b];
-        } while (iss.steps == 0);
-        iss.len = clamp_len(p, p.lens[iss.b]);
-      }
-      seek();
-    }
-  };
-
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) issue(s);
-
-  // ---- consume side
+  if (kShift) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+  // warp-major numbers: few workers then stand on as many SMs as they can
+  const int worker = warp * gridDim.x + blockIdx.x;
+  Stretch st = stretch_of<S, SPLIT>(p, s_prefix, worker);
+  if (SPLIT ? st.left <= 0 : st.cur.b < 0) return;
+  Cursor& cur = st.cur;
+  int64_t left = st.left;
+  uint8_t* const ring = smem + warp * (kStages * S::STAGE);
+  uint64_t* const full = s_full + warp * kStages;
+  uint64_t* const empty = s_empty + warp * kStages;
   int slot = 0;
   uint32_t parity = 0;
-  int64_t left = end - at;
   bool first_piece = true;
-  do {
+  while (true) {
     // one piece: steps [cur.step, stop) of one segment
     const int stop = static_cast<int>(min(static_cast<int64_t>(cur.steps), cur.step + left));
     const bool whole = cur.step == 0 && stop == cur.steps;
-    const int h = cur.z / p.groups, row0 = (cur.z % p.groups) * ROWS;
+    const int h = cur.z / p.groups, row0 = (cur.z - h * p.groups) * ROWS;
 
     // q as B fragments, its channels in the order of K's pieces
     uint32_t qf[NT][D / 16][2];
@@ -429,6 +532,62 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
           qf[n][ks + 1][1] = w.w;
         }
     }
+    float to_log2 = p.scale_log2;
+    float base_s[NT][2];  // where a score's sum starts
+#pragma unroll
+    for (int n = 0; n < NT; ++n) base_s[n][0] = base_s[n][1] = 0.f;
+    if (S::KB == 1) {
+      if (!std::is_same<T, TK>::value) {
+        // bf16 q to fp16, times the power of two that brings the largest of
+        // these rows to [2^13, 2^14): exact down to 2^-28 of it, and what is lost
+        // below is less than fp32 loses in the sum
+        float top = 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 f = unpack16<T>(qf[n][i][e]);
+              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+        top = warp_max(top);
+        const int ex = static_cast<int>(__float_as_uint(top) >> 23 & 255);
+        const int k = top > 0.f ? min(127, 13 - (ex - 127)) : 0;  // >= -114
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+        // 2^-k, in two factors: k = 127 has no normal reciprocal
+        to_log2 *= __uint_as_float(static_cast<uint32_t>(127 - k / 2) << 23);
+        to_log2 *= __uint_as_float(static_cast<uint32_t>(127 - (k - k / 2)) << 23);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 f = unpack16<T>(qf[n][i][e]);
+              qf[n][i][e] = pack16<__half>(f.x * up, f.y * up);
+            }
+      }
+      // code + 128, as the bits of an fp16 number, is (code + 128) 2^-24: the sums
+      // start at -128 2^-24 sum q, and end 2^24 times too small
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 f = unpack16<__half>(qf[n][i][e]);
+            sum += f.x + f.y;
+          }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);  // of row g
+        sum *= -128.f / 16777216.f;
+        base_s[n][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
+        base_s[n][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+      }
+      to_log2 *= 16777216.f;
+    }
     // keys visible to this lane's two rows of each tile
     int vis[NT][2];
     int vis_min = cur.len;
@@ -442,11 +601,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
       }
     if (p.causal) vis_min = cur.len - p.n_q + 1;
 
+    // m: largest score; mo: largest score + log2 delta_V (m without V scales),
+    // the unit that O is summed in; l: sum of 2^(s - m)
     float acc[NT][D / 16][4];
-    float m[NT][2], l[NT][2];
+    float m[NT][2], mo[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      m[n][0] = m[n][1] = -INFINITY;
+      m[n][0] = m[n][1] = mo[n][0] = mo[n][1] = -INFINITY;
       l[n][0] = l[n][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -455,34 +616,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
     }
 
     for (; cur.step < stop; ++cur.step, --left) {
-      __syncwarp();  // every lane is done with the stage that is filled next
-      {
-        int next = slot + kStages - 1;
-        if (next >= kStages) next -= kStages;
-        issue(next);
-      }
       uint8_t* const base = ring + slot * S::STAGE;
-      const bool there = mbar_wait(bar + slot, parity, s_abort + warp, p.timeout_ns, 0xD0);
-      if (!__all_sync(0xffffffffu, there)) {
-        // Given up (the error word says so).  The copies under way write to this
-        // CTA's memory: wait for them too, as long again at most.
-        const uint64_t since = globaltimer();
-        for (int64_t n = left; n > 0 && n > left - kStages; --n) {
-          while (!mbar_try_wait_hint(bar + slot, parity) && globaltimer() - since < p.timeout_ns) {
-          }
-          if (++slot == kStages) {
-            slot = 0;
-            parity ^= 1;
-          }
-        }
-        return;
-      }
+      const bool there = mbar_wait(full + slot, parity, &s_abort, p.timeout_ns, 0xD0);
+      if (!__all_sync(0xffffffffu, there)) return;  // given up: the error word says so
       const int t0 = cur.step * S::TOK;
-      const uint32_t gone = absent >> 4 * slot & 15;
-      if (++slot == kStages) {
-        slot = 0;
-        parity ^= 1;
-      }
+      const uint32_t gone = s_absent[warp * kStages + slot];
       // Behind the last token the page may hold anything, and a tile on no page
       // was not copied.  Their scores are masked below; their V is zeroed here,
       // since 0 * NaN would reach the sums.
@@ -490,7 +628,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
 #pragma unroll
         for (int u = 0; u < S::SUB; ++u) {
           const int have = gone >> u & 1 ? 0 : min(16, max(0, cur.len - t0 - 16 * u));
-          for (int i = 16 * (have * (S::VROW / 16) + lane); i < 16 * S::VROW; i += 512)
+          for (int i = have * S::VROW + 16 * lane; i < 16 * S::VROW; i += 512)
             *reinterpret_cast<uint4*>(base + S::V_AT + 16 * u * S::VROW + i) = make_uint4(0, 0, 0, 0);
           if (S::VS && lane >= have && lane < 16)
             *reinterpret_cast<float*>(base + S::VS_AT + (16 * u + lane) * 4) = 0.f;
@@ -499,7 +637,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
         __syncwarp();
       }
 
-      // ---- scores, in units of log2
+      // ---- sums of products with K
       float s[NT][S::SUB][4];
 #pragma unroll
       for (int u = 0; u < S::SUB; ++u) {
@@ -508,7 +646,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][u][e] = s2[n][e] = 0.f;
+          for (int e = 0; e < 4; ++e) {
+            s[n][u][e] = base_s[n][e & 1];
+            s2[n][e] = 0.f;
+          }
 #pragma unroll
         for (int x = 0; x < S::KC; ++x) {
           const uint4 w0 = *reinterpret_cast<const uint4*>(kb + x * 64);
@@ -519,36 +660,78 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
             for (int y = 0; y < 2; ++y) {
               const uint32_t a[4] = {a0[2 * y], a1[2 * y], a0[2 * y + 1], a1[2 * y + 1]};
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816<T>(y ? s2[n] : s[n][u], a, qf[n][2 * x + y][0], qf[n][2 * x + y][1]);
+              for (int n = 0; n < NT; ++n)
+                mma16816<TK>(y ? s2[n] : s[n][u], a, qf[n][2 * x + y][0], qf[n][2 * x + y][1]);
             }
           } else {
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               uint32_t a[4];
-              codes_to_16<T>(a0[y], a[0], a[2]);
-              codes_to_16<T>(a1[y], a[1], a[3]);
+              codes_to_half(a0[y], a[0], a[2]);
+              codes_to_half(a1[y], a[1], a[3]);
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                mma16816<T>(y & 1 ? s2[n] : s[n][u], a, qf[n][(4 * x + y) % (D / 16)][0],
-                            qf[n][(4 * x + y) % (D / 16)][1]);
+                mma16816<TK>(y & 1 ? s2[n] : s[n][u], a, qf[n][(4 * x + y) % (D / 16)][0],
+                             qf[n][(4 * x + y) % (D / 16)][1]);
             }
           }
         }
-        float f0 = p.scale_log2, f1 = p.scale_log2;
-        if (S::KS) {
-          const uint8_t* const sb = base + S::KS_AT + u * 64;
-          f0 *= *reinterpret_cast<const float*>(sb + g * 4);
-          f1 *= *reinterpret_cast<const float*>(sb + (g + 8) * 4);
-        }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          s[n][u][0] = (s[n][u][0] + s2[n][0]) * f0;
-          s[n][u][1] = (s[n][u][1] + s2[n][1]) * f0;
-          s[n][u][2] = (s[n][u][2] + s2[n][2]) * f1;
-          s[n][u][3] = (s[n][u][3] + s2[n][3]) * f1;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][u][e] += s2[n][e];
+      }
+      // ---- V to registers; the stage is free once all of it is
+      constexpr int VWORDS = S::VW / 4;
+      uint32_t vr[S::SUB][4][S::VC][VWORDS];
+      float ks[S::SUB][2], lv[S::SUB][2];
+#pragma unroll
+      for (int u = 0; u < S::SUB; ++u) {
+        const uint8_t* const vb = base + S::V_AT + (16 * u + 2 * c) * S::VROW + g * S::VW;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int x = 0; x < S::VC; ++x) {
+            const uint8_t* const v0 = vb + ((j & 1) + 8 * (j >> 1)) * S::VROW + x * 8 * S::VW;
+            if (S::VW == 16) {
+              const uint4 r = *reinterpret_cast<const uint4*>(v0);
+              vr[u][j][x][0] = r.x;
+              vr[u][j][x][1] = r.y;
+              vr[u][j][x][2 % VWORDS] = r.z;
+              vr[u][j][x][3 % VWORDS] = r.w;
+            } else {
+              const uint2 r = *reinterpret_cast<const uint2*>(v0);
+              vr[u][j][x][0] = r.x;
+              vr[u][j][x][1] = r.y;
+            }
+          }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          ks[u][e] = S::KS ? *reinterpret_cast<const float*>(base + S::KS_AT + (16 * u + 8 * e + g) * 4) : 1.f;
+          lv[u][e] = S::VS ? *reinterpret_cast<const float*>(base + S::VS_AT + (16 * u + 8 * e + g) * 4) : 1.f;
         }
       }
-      // ---- masks: the end of the cache, later query tokens' keys, bad pages
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + slot);
+      if (++slot == kStages) {
+        slot = 0;
+        parity ^= 1;
+      }
+
+      // ---- scores, in units of log2
+#pragma unroll
+      for (int u = 0; u < S::SUB; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float f = S::KS ? to_log2 * ks[u][e] : to_log2;
+          if (S::VS) lv[u][e] = log2_fast(lv[u][e]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            s[n][u][2 * e] *= f;
+            s[n][u][2 * e + 1] *= f;
+          }
+        }
+      // ---- masks: the end of the cache, later query tokens' keys, no page
       if (t0 + S::TOK > vis_min || gone != 0) {
 #pragma unroll
         for (int u = 0; u < S::SUB; ++u)
@@ -562,16 +745,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
       }
       // ---- running maxima: reduced over the lanes only when one grew
       bool grew = false;
-      float top[NT][2];
+      float top[NT][2], topo[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float t = fmaxf(s[n][0][e], s[n][0][e + 2]);
+          float t = -INFINITY, to = -INFINITY;
 #pragma unroll
-          for (int u = 1; u < S::SUB; ++u) t = fmaxf(t, fmaxf(s[n][u][e], s[n][u][e + 2]));
+          for (int u = 0; u < S::SUB; ++u) {
+            t = fmaxf(t, fmaxf(s[n][u][e], s[n][u][e + 2]));
+            if (S::VS) to = fmaxf(to, fmaxf(s[n][u][e] + lv[u][0], s[n][u][e + 2] + lv[u][1]));
+          }
           top[n][e] = t;
+          topo[n][e] = to;
           grew |= t > m[n][e];
+          if (S::VS) grew |= to > mo[n][e];
         }
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -579,14 +767,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
           float alpha[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float t = top[n][e];
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-            t = fmaxf(t, m[n][e]);
-            alpha[e] = t == m[n][e] ? 1.f : exp2_fast(m[n][e] - t);
+            float t = fmaxf(token_max(top[n][e]), m[n][e]);
+            const float a = t == m[n][e] ? 1.f : exp2_fast(m[n][e] - t);
             m[n][e] = t;
-            l[n][e] *= alpha[e];
+            l[n][e] *= a;
+            alpha[e] = a;
+            if (S::VS) {
+              t = fmaxf(token_max(topo[n][e]), mo[n][e]);
+              alpha[e] = t == mo[n][e] ? 1.f : exp2_fast(mo[n][e] - t);
+              mo[n][e] = t;
+            }
           }
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
@@ -598,112 +788,79 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
         }
       }
       // ---- probabilities and O^T += V^T P^T
+      uint32_t pf[NT][S::SUB][2];
 #pragma unroll
-      for (int u = 0; u < S::SUB; ++u) {
-        const uint8_t* const vb = base + S::V_AT + (16 * u + 2 * c) * S::VROW + g * S::VW;
-        uint32_t pf[NT][2];
-        float f0 = 1.f, f1 = 1.f;
-        if (S::VS) {
-          // fp16: times 448, i.e. the row's largest |v|, which fp16 can hold;
-          // delta_V itself would push small rows into fp16's subnormals
-          const float up = std::is_same<T, __half>::value ? 448.f : 1.f;
-          const uint8_t* const sb = base + S::VS_AT + u * 64;
-          f0 = *reinterpret_cast<const float*>(sb + g * 4) * up;
-          f1 = *reinterpret_cast<const float*>(sb + (g + 8) * 4) * up;
+      for (int n = 0; n < NT; ++n) {
+        float m0[2], mo0[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m0[e] = m[n][e] == -INFINITY ? 0.f : m[n][e];
+          mo0[e] = mo[n][e] == -INFINITY ? 0.f : mo[n][e];
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-          float e0 = exp2_fast(s[n][u][0] - m0), e1 = exp2_fast(s[n][u][1] - m1);
-          float e2 = exp2_fast(s[n][u][2] - m0), e3 = exp2_fast(s[n][u][3] - m1);
-          l[n][0] += e0 + e2;
-          l[n][1] += e1 + e3;
+        for (int u = 0; u < S::SUB; ++u) {
+          float e[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) e[i] = exp2_fast(s[n][u][i] - m0[i & 1]);
+          l[n][0] += e[0] + e[2];
+          l[n][1] += e[1] + e[3];
           if (S::VS) {
-            e0 *= f0;
-            e1 *= f0;
-            e2 *= f1;
-            e3 *= f1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = exp2_fast(s[n][u][i] + (lv[u][i >> 1] - mo0[i & 1]));
           }
-          pf[n][0] = transpose8x8(pack16<T>(e0, e1));
-          pf[n][1] = transpose8x8(pack16<T>(e2, e3));
+          pf[n][u][0] = transpose8x8(pack16<TV>(e[0], e[1]));
+          pf[n][u][1] = transpose8x8(pack16<TV>(e[2], e[3]));
         }
+      }
 #pragma unroll
-        for (int x = 0; x < S::VC; ++x) {
-          if (S::VB == 2) {
-            const uint8_t* const v0 = vb + x * 128;
-            const uint4 r0 = *reinterpret_cast<const uint4*>(v0);
-            const uint4 r1 = *reinterpret_cast<const uint4*>(v0 + S::VROW);
-            const uint4 r2 = *reinterpret_cast<const uint4*>(v0 + 8 * S::VROW);
-            const uint4 r3 = *reinterpret_cast<const uint4*>(v0 + 9 * S::VROW);
-            const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
-            const uint32_t w2[4] = {r2.x, r2.y, r2.z, r2.w}, w3[4] = {r3.x, r3.y, r3.z, r3.w};
+      for (int u = 0; u < S::SUB; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t a[4] = {bytes(w0[i], w1[i], 0x5410), bytes(w0[i], w1[i], 0x7632),
-                                     bytes(w2[i], w3[i], 0x5410), bytes(w2[i], w3[i], 0x7632)};
+        for (int x = 0; x < S::VC; ++x)
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816<T>(acc[n][(4 * x + i) % (D / 16)], a, pf[n][0], pf[n][1]);
-            }
-          } else {
-            uint32_t w[4][4];
+          for (int i = 0; i < VWORDS; ++i) {
+            const uint32_t w0 = vr[u][0][x][i], w1 = vr[u][1][x][i], w2 = vr[u][2][x][i], w3 = vr[u][3][x][i];
+            if (S::VB == 2) {
+              const uint32_t a[4] = {bytes(w0, w1, 0x5410), bytes(w0, w1, 0x7632), bytes(w2, w3, 0x5410),
+                                     bytes(w2, w3, 0x7632)};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint8_t* const v0 = vb + ((j & 1) + 8 * (j >> 1)) * S::VROW;
-              if (S::VW == 16) {
-                const uint4 r = *reinterpret_cast<const uint4*>(v0);
-                w[j][0] = r.x;
-                w[j][1] = r.y;
-                w[j][2] = r.z;
-                w[j][3] = r.w;
-              } else {
-                const uint2 r = *reinterpret_cast<const uint2*>(v0);
-                w[j][0] = r.x;
-                w[j][1] = r.y;
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < S::VW / 4; ++i) {
+              for (int n = 0; n < NT; ++n)
+                mma16816<TV>(acc[n][(VWORDS * x + i) % (D / 16)], a, pf[n][u][0], pf[n][u][1]);
+            } else {
               uint32_t x01[4], x23[4];
-              e4m3_pairs<T>(w[0][i], w[1][i], x01);
-              e4m3_pairs<T>(w[2][i], w[3][i], x23);
+              e4m3_pairs(w0, w1, x01);
+              e4m3_pairs(w2, w3, x23);
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 const uint32_t a[4] = {x01[2 * y], x01[2 * y + 1], x23[2 * y], x23[2 * y + 1]};
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                  mma16816<T>(acc[n][(2 * i + y) % (D / 16)], a, pf[n][0], pf[n][1]);
+                  mma16816<TV>(acc[n][(2 * (VWORDS * x + i) + y) % (D / 16)], a, pf[n][u][0], pf[n][u][1]);
               }
             }
           }
-        }
-      }
     }
 
     // ---- end of the piece
+    // Channels of a lane: VE neighbours of each of the VC pieces (a V piece's
+    // channels are spread over VE / 2 tiles, two a tile).
+    constexpr int TILES = S::VE / 2;
+    const int64_t slot_p = 2 * static_cast<int64_t>(worker) + (first_piece ? 0 : 1);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float t = l[n][e];
-        t += __shfl_xor_sync(0xffffffffu, t, 4);
-        t += __shfl_xor_sync(0xffffffffu, t, 8);
-        t += __shfl_xor_sync(0xffffffffu, t, 16);
-        l[n][e] = t;
-      }
-    const float down = S::VS && std::is_same<T, __half>::value ? 1.f / 448.f : 1.f;
-    // Channels of a lane: VE neighbours of each of the VC pieces (a V piece's
-    // channels are spread over VE / 2 tiles, two a tile).
-    constexpr int TILES = S::VE / 2;
-    if (!SPLIT || whole) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = row0 + 8 * n + 2 * c + e;
-          if (r >= p.rows) continue;
+        float sum = l[n][e];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int rg = 8 * n + 2 * c + e, r = row0 + rg;
+        if (r >= p.rows) continue;
+        // O to the unit of l
+        const float unit = S::VS && m[n][e] != -INFINITY ? exp2f(mo[n][e] - m[n][e]) : 1.f;
+        if (!SPLIT || whole) {
           const int qi = r / p.G, hh = h * p.G + (r - qi * p.G);
           const int64_t out = (static_cast<int64_t>(cur.b) * p.H + hh) * p.n_q + qi;
-          const float f = l[n][e] > 0.f ? down / l[n][e] : 0.f;
+          const float f = sum > 0.f ? unit / sum : 0.f;
           T* dst = reinterpret_cast<T*>(p.o) + out * D + g * S::VE;
 #pragma unroll
           for (int x = 0; x < S::VC; ++x)
@@ -716,123 +873,228 @@ __global__ void __launch_bounds__(kWarps * 32, 1) k_attn_decode(const DecodePara
               *reinterpret_cast<uint4*>(dst + x * 8 * S::VE + 2 * i) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           if (p.lse != nullptr && g == 0)
-            p.lse[out] = l[n][e] > 0.f ? (m[n][e] + log2f(l[n][e])) * 0.69314718055994531f : -INFINITY;
-        }
-    } else {
-      const int64_t slot_p = 2 * static_cast<int64_t>(worker) + (first_piece ? 0 : 1);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 8 * n + 2 * c + e;
-          if (row0 + r >= p.rows) continue;
-          float* dst = p.part_o + (slot_p * ROWS + r) * D + g * S::VE;
+            p.lse[out] = sum > 0.f ? (m[n][e] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+        } else {
+          float* dst = p.part_o + (slot_p * ROWS + rg) * D + g * S::VE;
 #pragma unroll
           for (int x = 0; x < S::VC; ++x)
 #pragma unroll
             for (int i = 0; i < TILES; i += 2)
               *reinterpret_cast<float4*>(dst + x * 8 * S::VE + 2 * i) =
-                  make_float4(acc[n][x * TILES + i][e] * down, acc[n][x * TILES + i][e + 2] * down,
-                              acc[n][x * TILES + i + 1][e] * down, acc[n][x * TILES + i + 1][e + 2] * down);
-          if (g == 0) p.part_ml[slot_p * ROWS + r] = make_float2(m[n][e], l[n][e]);
+                  make_float4(acc[n][x * TILES + i][e] * unit, acc[n][x * TILES + i][e + 2] * unit,
+                              acc[n][x * TILES + i + 1][e] * unit, acc[n][x * TILES + i + 1][e + 2] * unit);
+          if (g == 0) p.part_ml[slot_p * ROWS + rg] = make_float2(m[n][e], sum);
         }
-    }
+      }
     first_piece = false;
-    if (!SPLIT || left <= 0) break;
-    cur.step = 0;
-    if (++cur.z == HZ) {
-      cur.z = 0;
-      do {
-        ++cur.b;
-        cur.steps = s_prefix[cur.b + 1] - s_prefix[cur.b];
-      } while (cur.steps == 0);
-      cur.len = clamp_len(p, p.lens[cur.b]);
-    }
-  } while (true);
+    if (left <= 0) return;
+    next_segment(p, s_prefix, cur, left);
+    if (left <= 0) return;
+  }
 }
 
 // ------------------------------------------------------------------ join
-// One CTA per output row; its warps take the row's pieces in turn and are
-// joined in the order of the warps, so the sum's order is fixed.  Rows of
-// requests without tokens are zeros.
-constexpr int kJoinWarps = 4;
+// A CTA joins `per_cta` rows of one segment, all of which have the same n
+// pieces.  kJoinLoads pieces of O are in flight while the weights exp2(m_i - m)
+// are formed, and after that in each round.  Up to 32 pieces a warp joins
+// a row by itself; with more (or one row a CTA, where rows are few) the warps
+// share each row's pieces and are added in order.  Either way the order of the
+// sum depends on the sizes alone.  Rows of requests without tokens are zeros.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinLoads = 8;
+constexpr int kMaxPieces = kSms * kWarps;  // a segment has at most one of each worker
+
+// kJoinLoads pieces of a row (a lane's D / 32 channels of each): i0, i0 + stride, ...
+template <int D>
+__device__ __forceinline__ void load_pieces(float (*x)[D / 32], const float* po, int64_t piece, int late, int i0,
+                                            int stride, int n) {
+  constexpr int PER = D / 32;
+#pragma unroll
+  for (int j = 0; j < kJoinLoads; ++j) {
+    const int i = i0 + j * stride;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) x[j][e] = 0.f;
+    if (i < n) {
+      const float* src = po + (2 * i + (i == 0 ? late : 0)) * piece;
+      if (PER == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src);
+        x[j][0] = f.x;
+        x[j][1] = f.y;
+        x[j][PER - 2] = f.z;
+        x[j][PER - 1] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(src);
+        x[j][0] = f.x;
+        x[j][1] = f.y;
+      }
+    }
+  }
+}
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const DecodeParams p, int rows_per_group) {
+__global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const DecodeParams p, int rows_per_group, int per_cta,
+                                                                int parts) {
   constexpr int PER = D / 32;
+  __shared__ float s_w[kMaxPieces];
   __shared__ float s_o[kJoinWarps][D];
-  __shared__ float2 s_ml[kJoinWarps];
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int HZ = p.Hk * p.groups;
-  // grid: x = row of the group, y = kv head and group, z = request
-  const int r = blockIdx.x % p.rows, h = blockIdx.x / p.rows, b = blockIdx.y;
-  const int group = r / rows_per_group;
-  const int qi = r / p.G, hh = h * p.G + (r - qi * p.G);
-  const int64_t out = (static_cast<int64_t>(b) * p.H + hh) * p.n_q + qi;
+  // grid: x = segment of the request and part of its rows, y = request
+  const int z = blockIdx.x / parts, h = z / p.groups, row0 = (z - h * p.groups) * rows_per_group;
+  const int b = blockIdx.y;
+  const int first = (blockIdx.x - z * parts) * per_cta;
+  const int last = min(min(first + per_cta, rows_per_group), p.rows - row0);
+  if (first >= last) return;
+  // where row rg of the segment goes
+  auto out_of = [&](int rg) {
+    const int r = row0 + rg, qi = r / p.G;
+    return (static_cast<int64_t>(b) * p.H + h * p.G + (r - qi * p.G)) * p.n_q + qi;
+  };
+  // The lengths are inputs: the steps before this request and in all are
+  // counted while the pieces are still being computed.
+  int before = 0, all = 0;
+  for (int i = threadIdx.x; i < p.B; i += kJoinWarps * 32) {
+    const int v = places_of(clamp_len(p, p.lens[i]), p.step_tokens);
+    all += v;
+    if (i < b) before += v;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  __shared__ int2 s_steps[kJoinWarps];
+  if (lane == 0) s_steps[warp] = make_int2(before, all);
+  __syncthreads();
+  before = all = 0;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    before += s_steps[w].x;
+    all += s_steps[w].y;
+  }
+  const int places = places_of(clamp_len(p, p.lens[b]), p.step_tokens);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int steps = p.prefix[b + 1] - p.prefix[b];
-  T* dst = reinterpret_cast<T*>(p.o) + out * D;
-  if (steps == 0) {
-    for (int i = threadIdx.x; i < D; i += kJoinWarps * 32) dst[i] = T(0.f);
-    if (p.lse != nullptr && threadIdx.x == 0) p.lse[out] = -INFINITY;
+  if (places == 0) {
+    for (int rg = first + warp; rg < last; rg += kJoinWarps) {
+      const int64_t out = out_of(rg);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(p.o) + out * D);
+      for (int i = lane; i < D / 2; i += 32) dst[i] = 0;
+      if (p.lse != nullptr && lane == 0) p.lse[out] = -INFINITY;
+    }
     return;
   }
-  const int64_t total = static_cast<int64_t>(p.prefix[p.B]) * HZ;
-  const int64_t per = max(static_cast<int64_t>(kMinSteps), (total + p.workers - 1) / p.workers);
-  const int64_t s0 = static_cast<int64_t>(p.prefix[b]) * HZ + static_cast<int64_t>(h * p.groups + group) * steps;
-  const int64_t w0 = s0 / per, w1 = (s0 + steps - 1) / per;
-  if (w0 == w1) return;  // one piece: finished where it was computed
-  float m = -INFINITY, l = 0.f, o[PER];
+  const int64_t total = static_cast<int64_t>(all) * HZ;
+  const int64_t per = per_worker(total, p.workers);
+  const int64_t s0 = static_cast<int64_t>(before) * HZ + static_cast<int64_t>(z) * places;
+  const int w0 = static_cast<int>((s0 + kSegmentCost) / per), n = static_cast<int>((s0 + places - 1) / per) - w0 + 1;
+  if (n == 1) return;  // one piece: finished where it was computed
+  // a worker's first piece is in its first place, any other in its second
+  const int late = w0 * per < s0 ? 1 : 0;
+  const float2* ml = p.part_ml + static_cast<int64_t>(2 * w0) * rows_per_group;
+  const float* po = p.part_o + static_cast<int64_t>(2 * w0) * rows_per_group * D + lane * PER;
+  const int64_t piece = static_cast<int64_t>(rows_per_group) * D;
+
+  if (n <= (per_cta > 1 ? 32 : kJoinLoads)) {
+    for (int rg = first + warp; rg < last; rg += kJoinWarps) {
+      const float2 own = lane < n ? ml[(2 * lane + (lane == 0 ? late : 0)) * rows_per_group + rg]
+                                  : make_float2(-INFINITY, 0.f);
+      const float* row = po + static_cast<int64_t>(rg) * D;
+      float x[kJoinLoads][PER], o[PER];
+      load_pieces<D>(x, row, piece, late, 0, 1, n);
+      const float m = warp_max(own.x);
+      const float w = own.x == -INFINITY ? 0.f : exp2_fast(own.x - m);
+      const float l = warp_sum(own.y * w);
 #pragma unroll
-  for (int i = 0; i < PER; ++i) o[i] = 0.f;
-  const int rg = r - group * rows_per_group;
-  for (int64_t w = w0 + warp; w <= w1; w += kJoinWarps) {
-    // a worker's first piece is in its first place, any other in its second
-    const int64_t slot = 2 * w + (w == w0 && s0 != w0 * per ? 1 : 0);
-    const float2 ml = p.part_ml[slot * rows_per_group + rg];
-    const float* src = p.part_o + (slot * rows_per_group + rg) * D + lane * PER;
-    float x[PER];
-    if (PER == 4) {
-      const float4 f = *reinterpret_cast<const float4*>(src);
-      x[0] = f.x;
-      x[1] = f.y;
-      x[PER - 2] = f.z;
-      x[PER - 1] = f.w;
-    } else {
-      const float2 f = *reinterpret_cast<const float2*>(src);
-      x[0] = f.x;
-      x[1] = f.y;
+      for (int e = 0; e < PER; ++e) o[e] = 0.f;
+      for (int i0 = 0;;) {
+#pragma unroll
+        for (int j = 0; j < kJoinLoads; ++j) {
+          const float f = __shfl_sync(0xffffffffu, w, (i0 + j) & 31);
+#pragma unroll
+          for (int e = 0; e < PER; ++e) o[e] += f * x[j][e];
+        }
+        i0 += kJoinLoads;
+        if (i0 >= n) break;
+        load_pieces<D>(x, row, piece, late, i0, 1, n);
+      }
+      const float f = l > 0.f ? 1.f / l : 0.f;
+      const int64_t out = out_of(rg);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(p.o) + out * D + lane * PER);
+#pragma unroll
+      for (int e = 0; e < PER / 2; ++e) dst[e] = pack16<T>(o[2 * e] * f, o[2 * e + 1] * f);
+      if (p.lse != nullptr && lane == 0)
+        p.lse[out] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
-    const float t = fmaxf(m, ml.x);
-    if (t == -INFINITY) continue;  // nothing visible so far
-    const float fa = exp2_fast(m - t), fb = exp2_fast(ml.x - t);
-    l = l * fa + ml.y * fb;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] = o[i] * fa + x[i] * fb;
-    m = t;
+    return;
   }
-  if (lane == 0) s_ml[warp] = make_float2(m, l);
+
+  for (int rg = first; rg < last; ++rg) {
+    constexpr int kOwn = (kMaxPieces + kJoinWarps * 32 - 1) / (kJoinWarps * 32);
+    float2 own[kOwn];
+    float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) s_o[warp][lane * PER + i] = o[i];
-  __syncthreads();
-  if (threadIdx.x >= D / 2) return;
-  float mm = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) mm = fmaxf(mm, s_ml[w].x);
-  float ll = 0.f, a0 = 0.f, a1 = 0.f;
-  if (mm != -INFINITY) {
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      const float f = exp2_fast(s_ml[w].x - mm);
-      ll += s_ml[w].y * f;
-      a0 += s_o[w][2 * threadIdx.x] * f;
-      a1 += s_o[w][2 * threadIdx.x + 1] * f;
+    for (int j = 0; j < kOwn; ++j) {
+      const int i = threadIdx.x + j * kJoinWarps * 32;
+      own[j] = i < n ? ml[(2 * i + (i == 0 ? late : 0)) * rows_per_group + rg] : make_float2(-INFINITY, 0.f);
+      m = fmaxf(m, own[j].x);
     }
+    const float* row = po + static_cast<int64_t>(rg) * D;
+    float x[kJoinLoads][PER];
+    load_pieces<D>(x, row, piece, late, warp, kJoinWarps, n);
+    m = warp_max(m);
+    if (lane == 0) s_m[warp] = m;
+    __syncthreads();
+    m = warp_max(s_m[lane % kJoinWarps]);
+    float l = 0.f;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      const int i = threadIdx.x + j * kJoinWarps * 32;
+      if (i < n) {
+        const float w = own[j].x == -INFINITY ? 0.f : exp2_fast(own[j].x - m);
+        l += own[j].y * w;
+        s_w[i] = w;
+      }
+    }
+    l = warp_sum(l);
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    float o[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = 0.f;
+    for (int i0 = warp;;) {
+#pragma unroll
+      for (int j = 0; j < kJoinLoads; ++j) {
+        const int i = i0 + j * kJoinWarps;
+        const float f = i < n ? s_w[i] : 0.f;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) o[e] += f * x[j][e];
+      }
+      i0 += kJoinWarps * kJoinLoads;
+      if (i0 >= n) break;
+      load_pieces<D>(x, row, piece, late, i0, kJoinWarps, n);
+    }
+#pragma unroll
+    for (int e = 0; e < PER; ++e) s_o[warp][lane * PER + e] = o[e];
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+      float ll = 0.f, a0 = 0.f, a1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) {
+        ll += s_l[w];
+        a0 += s_o[w][2 * threadIdx.x];
+        a1 += s_o[w][2 * threadIdx.x + 1];
+      }
+      const float f = ll > 0.f ? 1.f / ll : 0.f;
+      const int64_t out = out_of(rg);
+      reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(p.o) + out * D)[threadIdx.x] = pack16<T>(a0 * f, a1 * f);
+      if (p.lse != nullptr && threadIdx.x == 0)
+        p.lse[out] = ll > 0.f ? (m + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+    }
+    // s_o and s_l are read above; the next row writes them after two barriers,
+    // s_m and s_w after its first or before it, when every thread is past here
+    __syncthreads();
   }
-  const float f = ll > 0.f ? 1.f / ll : 0.f;
-  reinterpret_cast<uint32_t*>(dst)[threadIdx.x] = pack16<T>(a0 * f, a1 * f);
-  if (p.lse != nullptr && threadIdx.x == 0)
-    p.lse[out] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ---------------------------------------------------------------- the plan
@@ -842,7 +1104,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const DecodeParam
 struct Plan {
   int nt, groups, step_tokens, workers, ctas;
   bool split;
-  size_t off_ml, off_prefix, bytes;
+  size_t off_ml, bytes;
 };
 
 int step_tokens(int d, int format) {
@@ -860,15 +1122,15 @@ Plan plan_of(int B, int H, int H_kv, int n_q, int d, int max_len, int format) {
   const int64_t segments = static_cast<int64_t>(B) * H_kv * P.groups;
   const int64_t most = static_cast<int64_t>(kSms) * kWarps;
   P.split = steps > 4;
-  int64_t workers = P.split ? std::min(most, (segments * steps + kMinSteps - 1) / kMinSteps) : segments;
+  int64_t workers =
+      P.split ? std::min(most, (segments * (steps + kSegmentCost) + kMinSteps - 1) / kMinSteps) : segments;
   P.workers = static_cast<int>(workers);
   P.ctas = static_cast<int>(P.split ? std::min<int64_t>(kSms, workers)
                                     : std::max<int64_t>(std::min<int64_t>(kSms, workers), (workers + kWarps - 1) / kWarps));
   if (P.split) {
     const size_t slots = 2 * static_cast<size_t>(workers) * 8 * P.nt;
     P.off_ml = slots * d * sizeof(float);
-    P.off_prefix = P.off_ml + slots * sizeof(float2);
-    P.bytes = (P.off_prefix + (static_cast<size_t>(B) + 1) * sizeof(int) + 255) / 256 * 256;
+    P.bytes = (P.off_ml + slots * sizeof(float2) + 255) / 256 * 256;
   }
   return P;
 }
@@ -883,10 +1145,17 @@ cudaError_t launch_one(const DecodeParams& p, const Plan& P, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kRing + (SPLIT ? (kMaxBatch + 1) * static_cast<int>(sizeof(int)) : 0));
   if (e != cudaSuccess) return e;
-  f<<<P.ctas, kWarps * 32, smem, st>>>(p);
+  f<<<P.ctas, (kWarps + kFeeders) * 32, smem, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess || !SPLIT) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.rows * p.Hk, p.B);
+  // A CTA takes all rows of a segment (with a CTA a row, 2048 rows of two to five
+  // pieces took 9 us where this takes 4), and fewer where that leaves SMs idle.
+  const int in_group = std::min(8 * NT, p.rows);
+  const int64_t segments = static_cast<int64_t>(p.groups) * p.Hk * p.B;
+  int per_cta = in_group;
+  while (per_cta > 1 && segments * ((in_group + per_cta - 1) / per_cta) < 2 * kSms) per_cta = (per_cta + 1) / 2;
+  const int parts = (in_group + per_cta - 1) / per_cta;
+  cfg.gridDim = dim3(parts * p.groups * p.Hk, p.B);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -894,7 +1163,7 @@ cudaError_t launch_one(const DecodeParams& p, const Plan& P, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_attn_join<T, D>, p, 8 * NT);
+  return cudaLaunchKernelEx(&cfg, k_attn_join<T, D>, p, 8 * NT, per_cta, parts);
 }
 
 template <typename T, int D, int FMT>
@@ -947,7 +1216,6 @@ cudaError_t launch_attn_decode(const DecodeArgs& a, cudaStream_t st) {
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     p.part_o = reinterpret_cast<float*>(ws);
     p.part_ml = reinterpret_cast<float2*>(ws + P.off_ml);
-    p.prefix = reinterpret_cast<int*>(ws + P.off_prefix);
   }
   p.num_pages = c.num_pages;
   p.page_size = c.page_size;
@@ -962,6 +1230,7 @@ cudaError_t launch_attn_decode(const DecodeArgs& a, cudaStream_t st) {
   p.max_len = c.num_pages > 0 ? a.max_len : 0;  // no page: no token
   p.causal = a.causal;
   p.workers = P.workers;
+  p.step_tokens = P.step_tokens;
   p.timeout_ns = a.timeout_ns;
   p.scale_log2 = a.sm_scale * 1.4426950408889634f;
   if (c.dtype == SAGE_F16)

@@ -214,8 +214,8 @@ sage_status_t check_decode_sizes(int B, int H, int H_kv, int n_q, int d, int max
   if (H % H_kv != 0) return SAGE_ERR_UNSUPPORTED;
   if (format != SAGE_KV_16 && format != SAGE_KV_B && format != SAGE_KV_8P8) return SAGE_ERR_UNSUPPORTED;
   if (B > 4096 || static_cast<long long>(n_q) * (H / H_kv) > 1024) return SAGE_ERR_UNSUPPORTED;
-  // steps of at least 16 tokens are counted in 32 bits
-  if (static_cast<long long>(B) * ((max_len + 15ll) / 16) > 0x7fffffffll) return SAGE_ERR_UNSUPPORTED;
+  // steps of at least 16 tokens, and two places more a request, are counted in 32 bits
+  if (static_cast<long long>(B) * ((max_len + 15ll) / 16 + 2) > 0x7fffffffll) return SAGE_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * H * (n_q > 0 ? n_q : 1) > 0x7fffffffll) return SAGE_ERR_UNSUPPORTED;
   return SAGE_OK;
 }
