@@ -293,7 +293,9 @@ sage_status_t sage_attn_fwd_varlen(const void* q, const void* k, const void* v, 
  * mean_k that the cache's K is smoothed by).  These entry points take fp16 and
  * bf16.  Lengths, tables, slots and positions are read on the device, so that
  * a step can be captured in a CUDA graph and replayed as the requests grow.
- * None of them allocates device memory or keeps state.
+ * None of them allocates device memory or keeps state.  Stride arrays are in
+ * host memory and read before the call returns; the stride of an axis of one
+ * entry is ignored.
  */
 typedef enum { SAGE_F16 = 0, SAGE_BF16 = 1 } sage_dtype_t;
 

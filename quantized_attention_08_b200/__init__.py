@@ -422,8 +422,9 @@ def sage_attn_fwd_varlen(q, k, v, cu_seqlens, max_seqlen: int, *, causal: bool =
 # ------------------------------------------------- serving from a paged cache
 KV_FORMATS = {"16": 0, "B": 1, "8+8": 2}
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
-_i64x2 = _c.c_int64 * 2
 _i64x3 = _c.c_int64 * 3
+_i64x4 = _c.c_int64 * 4
+_i64x14 = _c.c_int64 * 14
 
 
 class _CacheStruct(_c.Structure):
@@ -436,30 +437,26 @@ class _CacheStruct(_c.Structure):
 
 # The serving calls of a decode step take microseconds on the GPU, so their
 # checks keep to cheap accessors: device numbers for devices, torch's raw
-# stream lookup, and each library function looked up once.
-def _serving(t: torch.Tensor, dtype, name: str, dev: int):
-    """Checks of a serving argument (type, device number, last axis dense);
-    returns its strides, 0 for an axis of one entry (never used, and torch
-    may say anything there)."""
+# stream lookup, each library function looked up once, and outputs made like a
+# tensor that exists (a third of torch.empty's time).
+def _strided(t: torch.Tensor, dtype, name: str, dev: int):
+    """Checks of a strided argument (type, device number, last axis dense);
+    returns its strides."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
-    shape, st = t.shape, t.stride()
-    if 1 in shape:
-        st = [s if n > 1 else 0 for n, s in zip(shape, st)]
-        if shape and shape[-1] == 1:
-            st[-1] = 1
-    if shape and st[-1] != 1:
+    st = t.stride()
+    if not st or st[-1] != 1:
         raise ValueError(f"{name} must be dense along its last axis")
     return st
 
 
-def _ints(t: torch.Tensor, name: str, dev: int, shape) -> int:
-    """Checks of an int32 argument (type, device number, shape, contiguous);
-    returns its address."""
-    if t.dtype is not torch.int32:
-        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+def _dense(t: torch.Tensor, dtype, name: str, dev: int, shape) -> int:
+    """Checks of a contiguous argument (type, device number, shape); returns
+    its address."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     if t.shape != shape:
@@ -479,32 +476,25 @@ def _call(name: str, dev: int, *args):
     fn = _fns.get(name)
     if fn is None:
         fn = _fns[name] = getattr(load_library(), name)
-    st = torch._C._cuda_getCurrentRawStream(dev)
     if torch._C._cuda_getDevice() == dev:
-        status = fn(*args, st)
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, st)
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status:
         raise SageError(status, name)
 
 
-def _on_stream(f):
-    """A `stream` argument makes that stream current for the call, so that the
-    outputs and workspaces that torch hands out belong to it."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
-        dev = next(a.device for a in (*args, *kw.values()) if isinstance(a, torch.Tensor))
-        if not isinstance(stream, torch.cuda.Stream):
-            ptr = int(getattr(stream, "cuda_stream", stream))
-            stream = torch.cuda.ExternalStream(ptr, dev) if ptr else torch.cuda.default_stream(dev)
-        if stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-        with torch.cuda.stream(stream):
-            return f(*args, **kw)
-    return call
+def _with_stream(f, stream, t, *args, **kw):
+    """f with `stream` current, so that the outputs and workspaces that torch
+    hands out belong to it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        ptr = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(ptr, t.device) if ptr else torch.cuda.default_stream(t.device)
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    with torch.cuda.stream(stream):
+        return f(t, *args, **kw)
 
 
 class SageKVCache:
@@ -544,10 +534,9 @@ class SageKVCache:
                     raise ValueError(f"a cache of format {self.format} needs {name}")
                 continue
             if name.endswith("scale"):
-                _serving(t, torch.float32, name, self._dev)
-                if t.shape != k.shape[:3]:
-                    raise ValueError(f"{name} must be [num_pages, H_kv, page_size]")
-            elif t.device != self.device:
+                if t.dtype != torch.float32 or t.shape != k.shape[:3]:
+                    raise ValueError(f"{name} must be fp32 [num_pages, H_kv, page_size]")
+            if t.device != self.device:
                 raise ValueError(f"{name} must be on {self.device}")
             if self.num_pages and not t[0].is_contiguous():
                 raise ValueError(f"a page of {name} must be contiguous")
@@ -574,21 +563,23 @@ class SageKVCache:
                    scale() if format != "16" else None, scale() if format == "8+8" else None, dtype)
 
 
-@_on_stream
 def sage_kv_slots(ctx_lens, new_lens, free_pages, free_used, block_table, *, page_size: int, T: int,
-                  out=None):
+                  out=None, stream=None):
     """Block tables and slot maps of one step: ctx_lens, new_lens int32 [B],
     free_pages int32 [F] of which the first free_used (int32 [1]) are taken,
     block_table int32 [B, max_pages] (extended in place).  Returns (seq_lens
     [B], cu_seqlens [B+1], slot_map [T], positions [T], seq_ids [T],
     free_used [1]), all int32; `out` takes the same six tensors, of which
     seq_lens may be ctx_lens and free_used its input."""
-    dev = ctx_lens.get_device()
+    if stream is not None:
+        return _with_stream(sage_kv_slots, stream, ctx_lens, new_lens, free_pages, free_used, block_table,
+                            page_size=page_size, T=T, out=out)
+    i32, dev = torch.int32, ctx_lens.get_device()
     B, F, width = ctx_lens.numel(), free_pages.numel(), block_table.shape[-1]
     if out is None:
         if T < 0:
             raise ValueError("T must not be negative")
-        out = torch.empty(2 * B + 3 * T + 2, dtype=torch.int32, device=ctx_lens.device).split_with_sizes(
+        out = torch.empty(2 * B + 3 * T + 2, dtype=i32, device=ctx_lens.device).split_with_sizes(
             (B, B + 1, T, T, T, 1))
         lens = out[0].data_ptr()
         cu = lens + 4 * B
@@ -596,77 +587,94 @@ def sage_kv_slots(ctx_lens, new_lens, free_pages, free_used, block_table, *, pag
         pos, ids, used = slots + 4 * T, slots + 8 * T, slots + 12 * T
     else:
         lens, cu, slots, pos, ids, used = (
-            _ints(t, name, dev, (n,)) for t, name, n in
+            _dense(t, i32, name, dev, (n,)) for t, name, n in
             zip(out, ("seq_lens", "cu_seqlens", "slot_map", "positions", "seq_ids", "free_used"),
                 (B, B + 1, T, T, T, 1)))
-    _call("sage_kv_slots", dev, _ints(ctx_lens, "ctx_lens", dev, (B,)), _ints(new_lens, "new_lens", dev, (B,)), B,
-          _ints(free_pages, "free_pages", dev, (F,)), F, _ints(free_used, "free_used", dev, (1,)),
-          _ints(block_table, "block_table", dev, (B, width)), width, page_size, lens, cu, slots, pos, ids, T, used)
+    _call("sage_kv_slots", dev, _dense(ctx_lens, i32, "ctx_lens", dev, (B,)),
+          _dense(new_lens, i32, "new_lens", dev, (B,)), B, _dense(free_pages, i32, "free_pages", dev, (F,)), F,
+          _dense(free_used, i32, "free_used", dev, (1,)),
+          _dense(block_table, i32, "block_table", dev, (B, width)), width, page_size, lens, cu, slots, pos, ids, T, used)
     return out
 
 
-@_on_stream
-def sage_rope_axes(q, k, positions, inv_freq, sections, *, pairing: str = "half", q_out=None, k_out=None):
+def sage_rope_axes(q, k, positions, inv_freq, sections, *, pairing: str = "half", q_out=None, k_out=None,
+                   stream=None):
     """Rotary positions with several axes of q [B, H, N, d] and k [B, H_kv, N, d]
     (or [H, N, d] of one sequence; k may be None), any strides with a dense
     last axis.  positions int32 [axes, B, N] or [axes, N] (shared by the batch);
     sections: rotation pairs of each axis; inv_freq fp32 [sum(sections)];
     pairing "half" (i, i + R) or "interleaved" (2i, 2i + 1).  Returns (q, k)
-    rotated; q_out / k_out take them instead (they may be q and k)."""
-    dtype = q.dtype
+    rotated, laid out as torch.empty_like lays them out; q_out / k_out take
+    them instead (they may be q and k)."""
+    if stream is not None:
+        return _with_stream(sage_rope_axes, stream, q, k, positions, inv_freq, sections, pairing=pairing, q_out=q_out,
+                            k_out=k_out)
+    dtype, dev, shape = q.dtype, q.get_device(), q.shape
     code = _DTYPES.get(dtype)
     if code is None:
         raise TypeError(f"q must be torch.float16 or torch.bfloat16, got {dtype}")
-    if pairing not in ("half", "interleaved"):
+    if pairing != "half" and pairing != "interleaved":
         raise ValueError(f"pairing must be 'half' or 'interleaved', got {pairing!r}")
-    dev = q.get_device()
-    shape = q.shape
-    if len(shape) not in (3, 4):
+    if len(shape) == 4:
+        B, H, N, d = shape
+    elif len(shape) == 3:
+        B, (H, N, d) = 1, shape
+    else:
         raise ValueError("q must be [B, H, N, d] or [H, N, d]")
-    B = shape[0] if len(shape) == 4 else 1
-    H, N, d = shape[-3:]
 
-    def s3(t, like, name):
-        if t.shape != like:
-            raise ValueError(f"{name} does not have the shape of its input")
-        st = _serving(t, dtype, name, dev)
-        return _i64x3(*st[:3]) if len(st) == 4 else _i64x3(0, st[0], st[1])
-
+    # strides of q, q_out, k, k_out (batch, head, token) and positions, in one array
+    lead = () if len(shape) == 4 else (0,)
     if q_out is None:
-        q_out = torch.empty(shape, dtype=dtype, device=q.device)
-    Hk, kp, kop, ks, kos = 0, None, None, None, None
+        q_out = torch.empty_like(q)
+    elif q_out.shape != shape:
+        raise ValueError("q_out does not have the shape of its input")
+    st = (*lead, *_strided(q, dtype, "q", dev)[:-1], *lead, *_strided(q_out, dtype, "q_out", dev)[:-1])
     if k is not None:
         kshape = k.shape
-        if len(kshape) != len(shape) or kshape[-2:] != shape[-2:] or kshape[:-3] != shape[:-3]:
+        if len(kshape) != len(shape) or kshape[-2:] != shape[-2:] or (not lead and kshape[0] != B):
             raise ValueError("q and k must have the same batch, tokens and channels")
         if k_out is None:
-            k_out = torch.empty(kshape, dtype=dtype, device=q.device)
+            k_out = torch.empty_like(k)
+        elif k_out.shape != kshape:
+            raise ValueError("k_out does not have the shape of its input")
+        st += (*lead, *_strided(k, dtype, "k", dev)[:-1], *lead, *_strided(k_out, dtype, "k_out", dev)[:-1])
         Hk, kp, kop = kshape[-3], k.data_ptr(), k_out.data_ptr()
-        ks, kos = s3(k, kshape, "k"), s3(k_out, kshape, "k_out")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    A, R = len(sections), sum(sections)
-    ps = _serving(positions, torch.int32, "positions", dev)
-    if positions.shape != (A, B, N) and positions.shape != (A, N):
-        raise ValueError(f"positions must be [{A}, {N}] or [{A}, {B}, {N}], got {tuple(positions.shape)}")
-    _serving(inv_freq, torch.float32, "inv_freq", dev)
-    if inv_freq.shape != (R,):
-        raise ValueError(f"inv_freq must have {R} entries")
-    qs, qos = s3(q, shape, "q"), s3(q_out, shape, "q_out")
-    _call("sage_rope_axes", dev, q.data_ptr(), qs, q_out.data_ptr(), qos, kp, ks, kop, kos, positions.data_ptr(),
-          _i64x2(ps[0], ps[1] if len(ps) == 3 else 0), inv_freq.data_ptr(), (_i * A)(*sections), A, B, H, Hk, N, d,
-          pairing == "interleaved", code)
+    else:
+        Hk, kp, kop = 0, None, None
+        st += (0,) * 6
+    A = len(sections)
+    ps = _strided(positions, torch.int32, "positions", dev)
+    pshape = positions.shape
+    if pshape == (A, B, N):
+        st += ps[:2]
+    elif pshape == (A, N):
+        st += (ps[0], 0)
+    else:
+        raise ValueError(f"positions must be [{A}, {N}] or [{A}, {B}, {N}], got {tuple(pshape)}")
+    inv = _dense(inv_freq, torch.float32, "inv_freq", dev, (sum(sections),))
+    arr = _i64x14(*st)
+    at = _c.addressof(arr)
+    _call("sage_rope_axes", dev, q.data_ptr(), at, q_out.data_ptr(), at + 24, kp, at + 48, kop, at + 72,
+          positions.data_ptr(), at + 96, inv, _axes(tuple(sections)), A, B, H, Hk, N, d, pairing != "half", code)
     return q_out, k_out
 
 
-@_on_stream
-def sage_kv_append(k, v, slot_map, cache: SageKVCache, *, mean_k=None, seq_ids=None):
+@functools.lru_cache(maxsize=64)
+def _axes(sections):
+    return (_i * len(sections))(*sections)
+
+
+def sage_kv_append(k, v, slot_map, cache: SageKVCache, *, mean_k=None, seq_ids=None, stream=None):
     """Writes new K and V [H_kv, T, d] (any strides with a dense last axis) into
     the cache's slots slot_map int32 [T] (-1: skipped), quantized as the cache
     holds them.  mean_k fp32 [B, H_kv, d] with seq_ids int32 [T]: subtracted
     from K (Smooth K per request; every token of a request needs the same)."""
+    if stream is not None:
+        return _with_stream(sage_kv_append, stream, k, v, slot_map, cache, mean_k=mean_k, seq_ids=seq_ids)
     dev, shape = cache._dev, k.shape
-    ks, vs = _serving(k, cache.dtype, "k", dev), _serving(v, cache.dtype, "v", dev)
+    ks, vs = _strided(k, cache.dtype, "k", dev), _strided(v, cache.dtype, "v", dev)
     if len(shape) != 3 or v.shape != shape or shape[0] != cache.H_kv or shape[2] != cache.d:
         raise ValueError(f"k and v must both be [{cache.H_kv}, T, {cache.d}]")
     T = shape[1]
@@ -674,13 +682,13 @@ def sage_kv_append(k, v, slot_map, cache: SageKVCache, *, mean_k=None, seq_ids=N
     if mean_k is not None:
         if seq_ids is None:
             raise ValueError("mean_k needs seq_ids")
-        _serving(mean_k, torch.float32, "mean_k", dev)
         B = mean_k.shape[0]
-        if mean_k.shape != (B, cache.H_kv, cache.d) or not mean_k.is_contiguous():
-            raise ValueError(f"mean_k must be contiguous [B, {cache.H_kv}, {cache.d}]")
-        mean, ids = mean_k.data_ptr(), _ints(seq_ids, "seq_ids", dev, (T,))
-    _call("sage_kv_append", dev, k.data_ptr(), _i64x2(ks[0], ks[1]), v.data_ptr(), _i64x2(vs[0], vs[1]), T,
-          _ints(slot_map, "slot_map", dev, (T,)), mean, ids, B, cache._ref)
+        mean = _dense(mean_k, torch.float32, "mean_k", dev, (B, cache.H_kv, cache.d))
+        ids = _dense(seq_ids, torch.int32, "seq_ids", dev, (T,))
+    arr = _i64x4(ks[0], ks[1], vs[0], vs[1])
+    at = _c.addressof(arr)
+    _call("sage_kv_append", dev, k.data_ptr(), at, v.data_ptr(), at + 16, T,
+          _dense(slot_map, torch.int32, "slot_map", dev, (T,)), mean, ids, B, cache._ref)
     return cache
 
 
@@ -690,10 +698,14 @@ def sage_attn_decode_workspace_bytes(B: int, H: int, H_kv: int, n_q: int, d: int
         B, H, H_kv, n_q, d, max_len, KV_FORMATS[format] if isinstance(format, str) else int(format))
 
 
-@_on_stream
+@functools.lru_cache(maxsize=1024)
+def _decode_workspace(*sizes) -> int:
+    return load_library().sage_attn_decode_workspace_bytes(*sizes)
+
+
 def sage_attn_decode_paged(q, cache: SageKVCache, block_table, seq_lens, max_len: int, *,
                            causal: bool = True, sm_scale: Optional[float] = None, o=None,
-                           return_lse: bool = False, workspace: Optional[torch.Tensor] = None):
+                           return_lse: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
     """Attention of new tokens over the paged cache: q [B, H, n_q, d], or
     [B, H, d] of one token, any strides with a dense last axis; block_table
     int32 [B, max_pages], seq_lens int32 [B] (the new tokens included), max_len
@@ -701,28 +713,32 @@ def sage_attn_decode_paged(q, cache: SageKVCache, block_table, seq_lens, max_len
     last n_q are the new ones).  Returns o (dense, q's shape), or (o, lse fp32)
     with return_lse.  workspace: a tensor of at least
     sage_attn_decode_workspace_bytes() bytes; taken from torch if not given."""
+    if stream is not None:
+        return _with_stream(sage_attn_decode_paged, stream, q, cache, block_table, seq_lens, max_len, causal=causal,
+                            sm_scale=sm_scale, o=o, return_lse=return_lse, workspace=workspace)
     dev, d, shape = cache._dev, cache.d, q.shape
-    qs = _serving(q, cache.dtype, "q", dev)
-    if len(shape) == 4:
-        B, H, n_q, dq = shape
-        qs = _i64x3(qs[0], qs[1], qs[2])
-    elif len(shape) == 3:
-        B, H, dq = shape
-        n_q, qs = 1, _i64x3(qs[0], qs[1], 0)
+    qs = _strided(q, cache.dtype, "q", dev)
+    if len(shape) == 4 and shape[3] == d:
+        B, H, n_q, _ = shape
+        arr = _i64x3(qs[0], qs[1], qs[2])
+    elif len(shape) == 3 and shape[2] == d:
+        B, H, _ = shape
+        n_q = 1
+        arr = _i64x3(qs[0], qs[1], 0)
     else:
-        dq = -1
-    if dq != d:
         raise ValueError(f"q must be [B, H, n_q, {d}] or [B, H, {d}]")
     width = block_table.shape[-1]
     if o is None:
-        o = torch.empty(shape, dtype=q.dtype, device=q.device)
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+        op = o.data_ptr()
     else:
-        _serving(o, q.dtype, "o", dev)
-        if o.shape != shape or not o.is_contiguous():
-            raise ValueError("o must be contiguous and have q's shape")
-    lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device) if return_lse else None
+        op = _dense(o, q.dtype, "o", dev, shape)
+    lse, lp = None, None
+    if return_lse:
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+        lp = lse.data_ptr()
     if workspace is None:
-        size = sage_attn_decode_workspace_bytes(B, H, cache.H_kv, n_q, d, max_len, cache._struct.format)
+        size = _decode_workspace(B, H, cache.H_kv, n_q, d, max_len, cache._struct.format)
         ws = None
         if size:
             workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
@@ -731,10 +747,10 @@ def sage_attn_decode_paged(q, cache: SageKVCache, block_table, seq_lens, max_len
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     else:
         ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call("sage_attn_decode_paged", dev, q.data_ptr(), qs, cache._ref,
-          _ints(block_table, "block_table", dev, (B, width)), width, _ints(seq_lens, "seq_lens", dev, (B,)), B, H, n_q,
-          max_len, bool(causal), 1.0 / math.sqrt(d) if sm_scale is None else sm_scale, o.data_ptr(), _ptr(lse), ws,
-          size)
+    _call("sage_attn_decode_paged", dev, q.data_ptr(), arr, cache._ref,
+          _dense(block_table, torch.int32, "block_table", dev, (B, width)), width,
+          _dense(seq_lens, torch.int32, "seq_lens", dev, (B,)), B, H, n_q, max_len, 1 if causal else 0,
+          1.0 / math.sqrt(d) if sm_scale is None else sm_scale, op, lp, ws, size)
     return (o, lse) if return_lse else o
 
 

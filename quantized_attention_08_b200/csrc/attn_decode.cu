@@ -1141,9 +1141,11 @@ cudaError_t launch_one(const DecodeParams& p, const Plan& P, cudaStream_t st) {
   constexpr int kRing = kWarps * kStages * S::STAGE;
   const size_t smem = kRing + (SPLIT ? (static_cast<size_t>(p.B) + 1) * sizeof(int) : 0);
   auto* f = k_attn_decode<T, D, FMT, NT, SPLIT>;
-  // always the same value: calls of other host threads may set it too
-  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kRing + (SPLIT ? (kMaxBatch + 1) * static_cast<int>(sizeof(int)) : 0));
+  static OncePerDevice once;
+  cudaError_t e = once.run([&] {
+    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kRing + (SPLIT ? (kMaxBatch + 1) * static_cast<int>(sizeof(int)) : 0));
+  });
   if (e != cudaSuccess) return e;
   f<<<P.ctas, (kWarps + kFeeders) * 32, smem, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess || !SPLIT) return e;

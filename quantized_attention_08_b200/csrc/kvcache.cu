@@ -160,9 +160,11 @@ __global__ void __launch_bounds__(kSlotThreads) k_kv_slots(SlotArgs a) {
 cudaError_t launch_kv_slots(const SlotArgs& a, cudaStream_t st) {
   const size_t smem = (3 * static_cast<size_t>(a.B) + 2) * sizeof(int);
   if (smem > 32 * 1024) {
-    // always the same value: calls of other host threads may set it too
-    const cudaError_t e = cudaFuncSetAttribute(k_kv_slots, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (3 * kSlotMaxBatch + 2) * static_cast<int>(sizeof(int)));
+    static OncePerDevice once;
+    const cudaError_t e = once.run([&] {
+      return cudaFuncSetAttribute(k_kv_slots, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (3 * kSlotMaxBatch + 2) * static_cast<int>(sizeof(int)));
+    });
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

@@ -184,6 +184,9 @@ sage_status_t check_fwd_args(const void* q, const void* k, const void* v, void* 
   return SAGE_OK;
 }
 
+// The stride of an axis of one entry is never used: callers may leave anything there.
+int64_t stride_of(int64_t stride, int extent) { return extent > 1 ? stride : 0; }
+
 // A paged cache's sizes, strides and pointers.
 sage_status_t check_cache(const sage_kv_cache_t* c) {
   if (!c) return SAGE_ERR_INVALID_ARG;
@@ -867,8 +870,9 @@ sage_status_t sage_rope_axes(const void* q, const int64_t* q_strides, void* q_ou
   a.heads[1] = hk ? H_kv : 0;
   for (int w = 0; w < (hk ? 2 : 1); ++w)
     for (int i = 0; i < 3; ++i) {
-      a.in_s[w][i] = (w ? k_strides : q_strides)[i];
-      a.out_s[w][i] = (w ? k_out_strides : q_out_strides)[i];
+      const int extent = i == 0 ? B : i == 1 ? (w ? H_kv : H) : N;
+      a.in_s[w][i] = stride_of((w ? k_strides : q_strides)[i], extent);
+      a.out_s[w][i] = stride_of((w ? k_out_strides : q_out_strides)[i], extent);
       if (a.in_s[w][i] % 8 != 0 || a.out_s[w][i] % 8 != 0) return SAGE_ERR_MISALIGNED;
     }
   a.pos = positions;
@@ -900,9 +904,10 @@ sage_status_t sage_kv_append(const void* k, const int64_t* k_strides, const void
   if (!a16(k) || !a16(v) || !a4(slot_map) || !a16(mean_k) || !a4(seq_ids)) return SAGE_ERR_MISALIGNED;
   sage::AppendArgs a = {};
   for (int i = 0; i < 2; ++i) {
-    a.in_s[0][i] = k_strides[i];
-    a.in_s[1][i] = v_strides[i];
-    if (k_strides[i] % 8 != 0 || v_strides[i] % 8 != 0) return SAGE_ERR_MISALIGNED;
+    const int extent = i == 0 ? cache->H_kv : T;
+    a.in_s[0][i] = stride_of(k_strides[i], extent);
+    a.in_s[1][i] = stride_of(v_strides[i], extent);
+    if (a.in_s[0][i] % 8 != 0 || a.in_s[1][i] % 8 != 0) return SAGE_ERR_MISALIGNED;
   }
   a.in[0] = k;
   a.in[1] = v;
@@ -939,8 +944,8 @@ sage_status_t sage_attn_decode_paged(const void* q, const int64_t* q_strides,
   if (!a16(q) || !a16(o) || !a4(block_table) || !a4(seq_lens) || !a4(lse)) return SAGE_ERR_MISALIGNED;
   sage::DecodeArgs a = {};
   for (int i = 0; i < 3; ++i) {
-    a.q_s[i] = q_strides[i];
-    if (q_strides[i] % 8 != 0) return SAGE_ERR_MISALIGNED;
+    a.q_s[i] = stride_of(q_strides[i], i == 0 ? B : i == 1 ? H : n_q);
+    if (a.q_s[i] % 8 != 0) return SAGE_ERR_MISALIGNED;
   }
   const size_t need = sage::decode_workspace_bytes(B, H, cache->H_kv, n_q, cache->d, max_len, cache->format);
   if (need > 0) {

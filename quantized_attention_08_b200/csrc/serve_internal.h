@@ -5,9 +5,30 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "sage.h"
 
 namespace sage {
+
+// Runs a set-up call (one that may be repeated, with the same effect) on each
+// device's first use; a device whose call failed tries again.
+class OncePerDevice {
+ public:
+  template <typename F>
+  cudaError_t run(F f) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return f();
+    if (done_[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    if ((e = f()) == cudaSuccess) done_[dev].store(true, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  std::atomic<bool> done_[64] = {};
+};
 
 struct SlotArgs {
   const int32_t* ctx_lens;
