@@ -34,8 +34,8 @@
 // The order of k inside the products is free, so a lane's 16-byte pieces of
 // K's rows serve as fragments as they are; pairs of V's rows are interleaved
 // with prmt.  int8 and E4M3 codes become fp16 numbers exactly; delta_K multiplies
-// the fp32 scores, delta_V enters the exponents of the probabilities that
-// multiply V, which are then at most 1 whatever V's range.  S, m, l, O are fp32;
+// the fp32 scores, delta_V, in units of the largest one so far, the
+// probabilities.  S, m, l, O are fp32;
 // P is rounded to 16 bits for its product (2^-12 or 2^-9 relative, as every
 // 16-bit attention does), l sums the unrounded values.
 #include <cuda_bf16.h>
@@ -52,12 +52,28 @@ namespace sage {
 
 namespace {
 
+// the smallest scale a cache holds beside 0 (2^-100)
+constexpr float kTinyScale = 7.88860905e-31f;
 constexpr int kWarps = 8;
 constexpr int kStages = 3;
 constexpr int kFeeders = 4;   // loading warps
 constexpr int kMaxBatch = 4096;   // prefix sums in shared memory
 constexpr int kSms = 148;
 constexpr int kMinSteps = 2;      // of one warp's stretch
+// How the segments are spread over the warps.
+enum Mode {
+  kOne,     // a warp a segment
+  kLine,    // equal stretches of the line of all segments, joined by a second kernel
+  kCluster  // a cluster of CTAs a segment, joined through distributed shared memory
+};
+constexpr int kMaxCluster = 8;      // portable
+// A cluster a segment saves a launch and the workspace; it pays while a warp has
+// no more steps than this and all clusters find room at once (16 clusters of 8
+// did not: 19 us where the line takes 10).  One request, 8 kv heads, 16 bits:
+// 500 tokens 6.5 us against 8.2, 1009 8.6 against 8.9, 2048 10.1 against 9.2
+// (and a launch less on the host), 8192 17.8 against 14.0.
+constexpr int kClusterSteps = 2;
+constexpr int kClusterCtas = 128, kCluster8Ctas = 64;
 // What beginning a segment costs, in steps: the line counts each segment as that
 // much longer, so that a warp with many short ones gets fewer steps.
 constexpr int kSegmentCost = 2;
@@ -79,7 +95,7 @@ struct DecodeParams {
   float2* part_ml;               // [2 * workers][rows of a group]
   int num_pages, page_size, max_pages;
   int B, H, Hk, G, n_q, rows, groups;  // rows = G * n_q in `groups` groups of 8 NT
-  int max_len, causal, workers, step_tokens;
+  int max_len, causal, workers, step_tokens, cluster;
   float scale_log2;
   uint64_t timeout_ns;
 };
@@ -163,11 +179,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-__device__ __forceinline__ float log2_fast(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -220,9 +231,15 @@ inline __host__ __device__ int steps_of(int len, int tok) { return (len + tok - 
 // places of a segment in the line
 inline __host__ __device__ int places_of(int len, int tok) { return len > 0 ? steps_of(len, tok) + kSegmentCost : 0; }
 // places of a worker
-inline __host__ __device__ int64_t per_worker(int64_t total, int workers) {
-  const int64_t per = (total + workers - 1) / workers;
+// (at least total / workers; fp32 rounded up, since a 64-bit division is slow)
+__device__ __forceinline__ int64_t per_worker(int64_t total, int workers) {
+  const int64_t per = static_cast<int64_t>(ceilf(__fdiv_ru(__ll2float_ru(total), static_cast<float>(workers))));
   return per > kMinSteps ? per : kMinSteps;
+}
+
+// steps of a warp of a cluster
+__device__ __forceinline__ int cluster_steps(int steps, int cluster) {
+  return (steps + cluster * kWarps - 1) / (cluster * kWarps);
 }
 
 __device__ __forceinline__ int clamp_len(const DecodeParams& p, int len) {
@@ -246,66 +263,94 @@ struct Stretch {
   int64_t left;
 };
 
-template <typename S, bool SPLIT>
-__device__ __forceinline__ Stretch stretch_of(const DecodeParams& p, const int* s_prefix, int worker) {
+// The prefix sums of a CTA: places before each request, and how far into its
+// last step each one reaches (its length follows from the two).
+struct Requests {
+  const int* places;    // [B + 1]
+  const uint8_t* last;  // [B]
+};
+
+// Warp-major numbers: few workers then stand on as many SMs as they can.
+__device__ __forceinline__ int worker_of(int warp) { return warp * gridDim.x + blockIdx.x; }
+
+template <typename S, Mode MODE>
+__device__ __forceinline__ Stretch stretch_of(const DecodeParams& p, const Requests& q, int warp) {
   Stretch w;
   const int HZ = p.Hk * p.groups;
-  if (SPLIT) {
-    const int64_t total = static_cast<int64_t>(s_prefix[p.B]) * HZ;
+  w.left = 0;
+  w.cur.b = -1;
+  if (MODE == kLine) {
+    const int worker = worker_of(warp);
+    const int64_t total = static_cast<int64_t>(q.places[p.B]) * HZ;
     const int64_t per = per_worker(total, p.workers);
-    int64_t at = worker * per;
+    const int64_t at = worker * per;
     const int64_t end = worker < p.workers ? min(total, at + per) : 0;
-    w.left = 0;
     if (at >= end) return w;
-    // the request that holds place `at`: the last one with prefix * HZ <= at
+    // the request that holds place `at`: the last one with places * HZ <= at
     int lo = 0, hi = p.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (static_cast<int64_t>(s_prefix[mid]) * HZ <= at) lo = mid; else hi = mid;
+      if (static_cast<int64_t>(q.places[mid]) * HZ <= at) lo = mid; else hi = mid;
     }
-    const int places = s_prefix[lo + 1] - s_prefix[lo];
-    const int64_t in = at - static_cast<int64_t>(s_prefix[lo]) * HZ;
+    const int places = q.places[lo + 1] - q.places[lo];
+    int64_t in = at - static_cast<int64_t>(q.places[lo]) * HZ;
+    int z = static_cast<int>(__ll2float_rn(in) / static_cast<float>(places));  // off by one at most
+    z = min(z, HZ - 1);
+    in -= static_cast<int64_t>(z) * places;
+    if (in < 0) {
+      --z;
+      in += places;
+    } else if (in >= places) {
+      ++z;
+      in -= places;
+    }
+    const int place = static_cast<int>(in);
     w.cur.b = lo;
+    w.cur.z = z;
     w.cur.steps = places - kSegmentCost;
-    w.cur.z = static_cast<int>(in / places);
-    const int place = static_cast<int>(in - static_cast<int64_t>(w.cur.z) * places);
     w.cur.step = max(0, place - kSegmentCost);
-    w.cur.len = clamp_len(p, p.lens[lo]);
+    w.cur.len = (w.cur.steps - 1) * S::TOK + 1 + q.last[lo];
     // places at the segment's beginning that hold no step
     w.left = end - at - max(0, kSegmentCost - place);
-  } else {  // a segment a worker
-    w.left = 0;
-    w.cur.b = -1;
-    if (worker >= p.B * HZ) return w;
-    w.cur.b = worker / HZ;
-    w.cur.z = worker - w.cur.b * HZ;
+  } else {
+    const int segment = MODE == kOne ? worker_of(warp) : blockIdx.x / p.cluster;
+    if (segment >= p.B * HZ) return w;
+    w.cur.b = segment / HZ;
+    w.cur.z = segment - w.cur.b * HZ;
     w.cur.step = 0;
     w.cur.len = clamp_len(p, p.lens[w.cur.b]);
     w.cur.steps = steps_of(w.cur.len, S::TOK);
     w.left = w.cur.steps;
+    if (MODE == kCluster) {  // its warps take equal stretches, first those of the first warps
+      const int per = cluster_steps(w.cur.steps, p.cluster);
+      w.cur.step = (warp * p.cluster + blockIdx.x % p.cluster) * per;
+      w.left = max(0, min(per, w.cur.steps - w.cur.step));
+    }
   }
   return w;
 }
 
 // On to the next segment that has steps (the caller knows that places are left
 // beyond this one); those it has without a step are taken off `left`.
-__device__ __forceinline__ void next_segment(const DecodeParams& p, const int* s_prefix, Cursor& c, int64_t& left) {
+template <typename S>
+__device__ __forceinline__ void next_segment(const DecodeParams& p, const Requests& q, Cursor& c, int64_t& left) {
   left -= kSegmentCost;
   c.step = 0;
   if (++c.z < p.Hk * p.groups) return;
   c.z = 0;
+  if (left <= 0) return;
   do {
     ++c.b;
-    c.steps = s_prefix[c.b + 1] - s_prefix[c.b] - kSegmentCost;
+    c.steps = q.places[c.b + 1] - q.places[c.b] - kSegmentCost;
   } while (c.steps <= 0);
-  c.len = clamp_len(p, p.lens[c.b]);
+  c.len = (c.steps - 1) * S::TOK + 1 + q.last[c.b];
 }
 
 // The loading warp: lane w feeds the ring of warp w, so that one instruction
 // stream serves all of them.  The page numbers of a lane's next step are read
 // while the current one is copied.
-template <typename S, bool SPLIT>
-__device__ __forceinline__ void feed(const DecodeParams& p, const int* s_prefix, uint8_t* smem, uint64_t* full,
+template <typename S, Mode MODE>
+__device__ __forceinline__ void feed(const DecodeParams& p, const Requests& q, uint8_t* smem, uint64_t* full,
                                      uint64_t* empty, uint32_t* absent, volatile int* abort_flag, int feeder,
                                      int lane) {
   Stretch w;
@@ -318,7 +363,7 @@ __device__ __forceinline__ void feed(const DecodeParams& p, const int* s_prefix,
   const bool one_page = p.page_size % S::TOK == 0;  // a step lies in one page
   const int feeders = (one_page ? 1 : S::SUB) * (2 + S::KS + S::VS) <= 2 ? 1 : kFeeders;
   const int of = feeder < feeders ? feeder + lane * feeders : kWarps;  // the warp that this lane feeds
-  if (of < kWarps) w = stretch_of<S, SPLIT>(p, s_prefix, of * gridDim.x + blockIdx.x);
+  if (of < kWarps) w = stretch_of<S, MODE>(p, q, of);
   int64_t left = w.left;
   int issued = 0;  // stages filled, kStages at most
   uint8_t* const ring = smem + of * (kStages * S::STAGE);
@@ -395,7 +440,7 @@ __device__ __forceinline__ void feed(const DecodeParams& p, const int* s_prefix,
           ++tile_page;
         }
         if (++c.step == c.steps) {
-          next_segment(p, s_prefix, c, left);
+          next_segment<S>(p, q, c, left);
           seek();
         }
         if (left > 0) fetch();
@@ -435,7 +480,84 @@ __device__ __forceinline__ void feed(const DecodeParams& p, const int* s_prefix,
   }
 }
 
-template <typename T, int D, int FMT, int NT, bool SPLIT>
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address of this CTA's shared address `a` in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t a, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+
+// Joins the pieces that the consuming warps of a cluster have left in their rings
+// (O [ROWS][D] and (m, l) [ROWS] each; the first warps hold all the steps).
+// Sixteen lanes share four channels of a row, each of them a sixteenth of the
+// pieces; the CTAs of the cluster take turns at the channels.
+template <typename T, int D, int ROWS>
+__device__ __forceinline__ void join_cluster(const DecodeParams& p, int b, int h, int row0, int steps, uint8_t* smem,
+                                             int ring_bytes) {
+  cluster_barrier();
+  const int rows = min(ROWS, p.rows - row0);
+  const int per = cluster_steps(steps, p.cluster);
+  const int pieces = steps > 0 ? (steps + per - 1) / per : 0;
+  const uint32_t base = smem_u32(smem);
+  const int sub = threadIdx.x & 15;
+  const int rank = blockIdx.x % p.cluster;
+  const int units = rows * (D / 4);  // of four channels
+  for (int u0 = rank; u0 < units; u0 += p.cluster * (kWarps * 2)) {
+    const int u = u0 + (threadIdx.x >> 4) * p.cluster;
+    const bool in = u < units;
+    const int r = in ? u / (D / 4) : 0, ch = in ? (u - r * (D / 4)) * 4 : 0;
+    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int kMost = kMaxCluster * kWarps / 16;  // pieces of a lane
+    float ml[kMost][2], x[kMost][4];
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+      const int i = sub + 16 * j;
+      ml[j][0] = -INFINITY;
+      ml[j][1] = x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
+      if (in && i < pieces) {
+        const int w = i / p.cluster;
+        const uint32_t a = cluster_addr(base + w * ring_bytes, i - w * p.cluster);
+        asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
+                     : "=f"(ml[j][0]), "=f"(ml[j][1])
+                     : "r"(a + ROWS * D * 4 + r * 8));
+        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(x[j][0]), "=f"(x[j][1]), "=f"(x[j][2]), "=f"(x[j][3])
+                     : "r"(a + (r * D + ch) * 4));
+      }
+      m = fmaxf(m, ml[j][0]);
+    }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+      const float f = ml[j][0] == -INFINITY ? 0.f : exp2_fast(ml[j][0] - m);
+      l += ml[j][1] * f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] += x[j][e] * f;
+    }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, d);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] += __shfl_xor_sync(0xffffffffu, o[e], d);
+    }
+    if (in && sub == 0) {
+      const int row = row0 + r, qi = row / p.G;
+      const int64_t out = (static_cast<int64_t>(b) * p.H + h * p.G + (row - qi * p.G)) * p.n_q + qi;
+      const float f = l > 0.f ? 1.f / l : 0.f;
+      *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.o) + out * D + ch) =
+          make_uint2(pack16<T>(o[0] * f, o[1] * f), pack16<T>(o[2] * f, o[3] * f));
+      if (p.lse != nullptr && ch == 0)
+        p.lse[out] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
+  }
+  cluster_barrier();  // no CTA leaves while another reads its memory
+}
+
+template <typename T, int D, int FMT, int NT, Mode MODE>
 __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(const DecodeParams p) {
   using S = Step<D, FMT>;
   // int8 K and E4M3 V become fp16 whatever the model's type is
@@ -449,7 +571,9 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
   __shared__ int s_abort;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  int* s_prefix = reinterpret_cast<int*>(smem + kWarps * kStages * S::STAGE);  // SPLIT only: [B + 1]
+  int* s_places = reinterpret_cast<int*>(smem + kWarps * kStages * S::STAGE);  // kLine only
+  uint8_t* s_last = reinterpret_cast<uint8_t*>(s_places + p.B + 1);
+  const Requests q = {s_places, s_last};
 
   if (threadIdx.x < kWarps * kStages) {
     mbar_init(s_full + threadIdx.x, 1);
@@ -457,13 +581,14 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
     fence_mbar_init();
   }
   if (threadIdx.x == 0) s_abort = 0;
-  if (SPLIT) {
+  if (MODE == kLine) {
     // the join's CTAs may be placed now; they wait for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int run = 0;
     for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
       const int b = b0 + threadIdx.x;
-      int v = b < p.B ? places_of(clamp_len(p, p.lens[b]), S::TOK) : 0;
+      const int len = b < p.B ? clamp_len(p, p.lens[b]) : 0;
+      int v = places_of(len, S::TOK);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, v, o);
@@ -477,9 +602,12 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
         if (w < warp) before += s_scan[w];
         run += s_scan[w];
       }
-      if (b < p.B) s_prefix[b + 1] = before + v;
+      if (b < p.B) {
+        s_places[b + 1] = before + v;
+        s_last[b] = static_cast<uint8_t>((len - 1) % S::TOK);
+      }
     }
-    if (threadIdx.x == 0) s_prefix[0] = 0;
+    if (threadIdx.x == 0) s_places[0] = 0;
   }
   __syncthreads();
   // Two tiles of rows need more registers than 12 warps get at launch: the four
@@ -487,15 +615,13 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
   constexpr bool kShift = NT > 1;
   if (warp >= kWarps) {
     if (kShift) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    feed<S, SPLIT>(p, s_prefix, smem, s_full, s_empty, s_absent, &s_abort, warp - kWarps, lane);
+    feed<S, MODE>(p, q, smem, s_full, s_empty, s_absent, &s_abort, warp - kWarps, lane);
     return;
   }
 
   if (kShift) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-  // warp-major numbers: few workers then stand on as many SMs as they can
-  const int worker = warp * gridDim.x + blockIdx.x;
-  Stretch st = stretch_of<S, SPLIT>(p, s_prefix, worker);
-  if (SPLIT ? st.left <= 0 : st.cur.b < 0) return;
+  Stretch st = stretch_of<S, MODE>(p, q, warp);
+  if (MODE == kLine ? st.left <= 0 : st.cur.b < 0) return;
   Cursor& cur = st.cur;
   int64_t left = st.left;
   uint8_t* const ring = smem + warp * (kStages * S::STAGE);
@@ -507,7 +633,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
   while (true) {
     // one piece: steps [cur.step, stop) of one segment
     const int stop = static_cast<int>(min(static_cast<int64_t>(cur.steps), cur.step + left));
-    const bool whole = cur.step == 0 && stop == cur.steps;
+    const bool whole = MODE == kOne || (cur.step == 0 && stop == cur.steps);
     const int h = cur.z / p.groups, row0 = (cur.z - h * p.groups) * ROWS;
 
     // q as B fragments, its channels in the order of K's pieces
@@ -601,13 +727,15 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
       }
     if (p.causal) vis_min = cur.len - p.n_q + 1;
 
-    // m: largest score; mo: largest score + log2 delta_V (m without V scales),
-    // the unit that O is summed in; l: sum of 2^(s - m)
+    // m: largest score; l: sum of 2^(s - m).  O is summed in units of `unit`, the
+    // largest delta_V so far: P delta_V / unit is at most 1, whatever V's range, and
+    // what it loses below fp16's normal numbers is 2^-25 of the largest row of V.
     float acc[NT][D / 16][4];
-    float m[NT][2], mo[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2];
+    float unit = S::VS ? kTinyScale : 1.f, per_unit = S::VS ? 1.f / kTinyScale : 1.f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      m[n][0] = m[n][1] = mo[n][0] = mo[n][1] = -INFINITY;
+      m[n][0] = m[n][1] = -INFINITY;
       l[n][0] = l[n][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
@@ -618,7 +746,10 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
     for (; cur.step < stop; ++cur.step, --left) {
       uint8_t* const base = ring + slot * S::STAGE;
       const bool there = mbar_wait(full + slot, parity, &s_abort, p.timeout_ns, 0xD0);
-      if (!__all_sync(0xffffffffu, there)) return;  // given up: the error word says so
+      if (!__all_sync(0xffffffffu, there)) {  // given up: the error word says so
+        if (MODE != kCluster) return;
+        break;  // the other CTAs of the cluster will read this one's memory
+      }
       const int t0 = cur.step * S::TOK;
       const uint32_t gone = s_absent[warp * kStages + slot];
       // Behind the last token the page may hold anything, and a tile on no page
@@ -684,7 +815,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
       // ---- V to registers; the stage is free once all of it is
       constexpr int VWORDS = S::VW / 4;
       uint32_t vr[S::SUB][4][S::VC][VWORDS];
-      float ks[S::SUB][2], lv[S::SUB][2];
+      float ks[S::SUB][2], vs[S::SUB][2];
 #pragma unroll
       for (int u = 0; u < S::SUB; ++u) {
         const uint8_t* const vb = base + S::V_AT + (16 * u + 2 * c) * S::VROW + g * S::VW;
@@ -708,7 +839,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           ks[u][e] = S::KS ? *reinterpret_cast<const float*>(base + S::KS_AT + (16 * u + 8 * e + g) * 4) : 1.f;
-          lv[u][e] = S::VS ? *reinterpret_cast<const float*>(base + S::VS_AT + (16 * u + 8 * e + g) * 4) : 1.f;
+          vs[u][e] = S::VS ? *reinterpret_cast<const float*>(base + S::VS_AT + (16 * u + 8 * e + g) * 4) : 1.f;
         }
       }
       __syncwarp();
@@ -724,7 +855,6 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float f = S::KS ? to_log2 * ks[u][e] : to_log2;
-          if (S::VS) lv[u][e] = log2_fast(lv[u][e]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             s[n][u][2 * e] *= f;
@@ -745,38 +875,40 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
       }
       // ---- running maxima: reduced over the lanes only when one grew
       bool grew = false;
-      float top[NT][2], topo[NT][2];
+      float top[NT][2], top_v = 0.f;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float t = -INFINITY, to = -INFINITY;
+          float t = fmaxf(s[n][0][e], s[n][0][e + 2]);
 #pragma unroll
-          for (int u = 0; u < S::SUB; ++u) {
-            t = fmaxf(t, fmaxf(s[n][u][e], s[n][u][e + 2]));
-            if (S::VS) to = fmaxf(to, fmaxf(s[n][u][e] + lv[u][0], s[n][u][e + 2] + lv[u][1]));
-          }
+          for (int u = 1; u < S::SUB; ++u) t = fmaxf(t, fmaxf(s[n][u][e], s[n][u][e + 2]));
           top[n][e] = t;
-          topo[n][e] = to;
           grew |= t > m[n][e];
-          if (S::VS) grew |= to > mo[n][e];
         }
+      if (S::VS) {
+#pragma unroll
+        for (int u = 0; u < S::SUB; ++u) top_v = fmaxf(top_v, fmaxf(vs[u][0], vs[u][1]));
+        grew |= top_v > unit;
+      }
       if (__any_sync(0xffffffffu, grew)) {
+        float down = 1.f;
+        if (S::VS) {
+          top_v = fmaxf(token_max(top_v), unit);
+          per_unit = __frcp_rn(top_v);
+          down = unit * per_unit;
+          unit = top_v;
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float alpha[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float t = fmaxf(token_max(top[n][e]), m[n][e]);
-            const float a = t == m[n][e] ? 1.f : exp2_fast(m[n][e] - t);
+            const float t = fmaxf(token_max(top[n][e]), m[n][e]);
+            alpha[e] = t == m[n][e] ? 1.f : exp2_fast(m[n][e] - t);
             m[n][e] = t;
-            l[n][e] *= a;
-            alpha[e] = a;
-            if (S::VS) {
-              t = fmaxf(token_max(topo[n][e]), mo[n][e]);
-              alpha[e] = t == mo[n][e] ? 1.f : exp2_fast(mo[n][e] - t);
-              mo[n][e] = t;
-            }
+            l[n][e] *= alpha[e];
+            if (S::VS) alpha[e] *= down;
           }
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
@@ -791,12 +923,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
       uint32_t pf[NT][S::SUB][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float m0[2], mo0[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          m0[e] = m[n][e] == -INFINITY ? 0.f : m[n][e];
-          mo0[e] = mo[n][e] == -INFINITY ? 0.f : mo[n][e];
-        }
+        const float m0[2] = {m[n][0] == -INFINITY ? 0.f : m[n][0], m[n][1] == -INFINITY ? 0.f : m[n][1]};
 #pragma unroll
         for (int u = 0; u < S::SUB; ++u) {
           float e[4];
@@ -805,8 +932,9 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
           l[n][0] += e[0] + e[2];
           l[n][1] += e[1] + e[3];
           if (S::VS) {
+            const float f[2] = {vs[u][0] * per_unit, vs[u][1] * per_unit};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = exp2_fast(s[n][u][i] + (lv[u][i >> 1] - mo0[i & 1]));
+            for (int i = 0; i < 4; ++i) e[i] *= f[i >> 1];
           }
           pf[n][u][0] = transpose8x8(pack16<TV>(e[0], e[1]));
           pf[n][u][1] = transpose8x8(pack16<TV>(e[2], e[3]));
@@ -844,7 +972,11 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
     // Channels of a lane: VE neighbours of each of the VC pieces (a V piece's
     // channels are spread over VE / 2 tiles, two a tile).
     constexpr int TILES = S::VE / 2;
-    const int64_t slot_p = 2 * static_cast<int64_t>(worker) + (first_piece ? 0 : 1);
+    // where an unfinished piece goes: the workspace, or the warp's own ring
+    const int64_t slot_p = 2 * static_cast<int64_t>(worker_of(warp)) + (first_piece ? 0 : 1);
+    float* const part_o = MODE == kCluster ? reinterpret_cast<float*>(ring) : p.part_o + slot_p * ROWS * D;
+    float2* const part_ml =
+        MODE == kCluster ? reinterpret_cast<float2*>(ring + ROWS * D * sizeof(float)) : p.part_ml + slot_p * ROWS;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -855,9 +987,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const int rg = 8 * n + 2 * c + e, r = row0 + rg;
         if (r >= p.rows) continue;
-        // O to the unit of l
-        const float unit = S::VS && m[n][e] != -INFINITY ? exp2f(mo[n][e] - m[n][e]) : 1.f;
-        if (!SPLIT || whole) {
+        if (MODE == kOne || (MODE == kLine && whole)) {
           const int qi = r / p.G, hh = h * p.G + (r - qi * p.G);
           const int64_t out = (static_cast<int64_t>(cur.b) * p.H + hh) * p.n_q + qi;
           const float f = sum > 0.f ? unit / sum : 0.f;
@@ -875,7 +1005,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
           if (p.lse != nullptr && g == 0)
             p.lse[out] = sum > 0.f ? (m[n][e] + log2f(sum)) * 0.69314718055994531f : -INFINITY;
         } else {
-          float* dst = p.part_o + (slot_p * ROWS + rg) * D + g * S::VE;
+          float* dst = part_o + rg * D + g * S::VE;
 #pragma unroll
           for (int x = 0; x < S::VC; ++x)
 #pragma unroll
@@ -883,12 +1013,16 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
               *reinterpret_cast<float4*>(dst + x * 8 * S::VE + 2 * i) =
                   make_float4(acc[n][x * TILES + i][e] * unit, acc[n][x * TILES + i][e + 2] * unit,
                               acc[n][x * TILES + i + 1][e] * unit, acc[n][x * TILES + i + 1][e + 2] * unit);
-          if (g == 0) p.part_ml[slot_p * ROWS + rg] = make_float2(m[n][e], sum);
+          if (g == 0) part_ml[rg] = make_float2(m[n][e], sum);
         }
       }
+    if (MODE == kCluster) {
+      join_cluster<T, D, ROWS>(p, cur.b, h, row0, cur.steps, smem, kStages * S::STAGE);
+      return;
+    }
     first_piece = false;
     if (left <= 0) return;
-    next_segment(p, s_prefix, cur, left);
+    next_segment<S>(p, q, cur, left);
     if (left <= 0) return;
   }
 }
@@ -1102,8 +1236,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const DecodeParam
 // device): how many query rows a warp takes, whether segments are split, and
 // how many workers share the line.
 struct Plan {
-  int nt, groups, step_tokens, workers, ctas;
-  bool split;
+  int nt, groups, step_tokens, workers, ctas, cluster;
+  Mode mode;
   size_t off_ml, bytes;
 };
 
@@ -1120,14 +1254,22 @@ Plan plan_of(int B, int H, int H_kv, int n_q, int d, int max_len, int format) {
   P.step_tokens = step_tokens(d, format);
   const int64_t steps = steps_of(max_len, P.step_tokens);
   const int64_t segments = static_cast<int64_t>(B) * H_kv * P.groups;
-  const int64_t most = static_cast<int64_t>(kSms) * kWarps;
-  P.split = steps > 4;
-  int64_t workers =
-      P.split ? std::min(most, (segments * (steps + kSegmentCost) + kMinSteps - 1) / kMinSteps) : segments;
-  P.workers = static_cast<int>(workers);
-  P.ctas = static_cast<int>(P.split ? std::min<int64_t>(kSms, workers)
-                                    : std::max<int64_t>(std::min<int64_t>(kSms, workers), (workers + kWarps - 1) / kWarps));
-  if (P.split) {
+  int cluster = kMaxCluster;
+  while (cluster > 1 && segments * cluster > (cluster == 8 ? kCluster8Ctas : kClusterCtas)) cluster /= 2;
+  if (steps <= 4) {
+    P.mode = kOne;
+    P.workers = static_cast<int>(segments);
+    P.ctas = static_cast<int>(std::max<int64_t>(std::min<int64_t>(kSms, segments), (segments + kWarps - 1) / kWarps));
+  } else if (cluster > 1 && steps <= static_cast<int64_t>(kClusterSteps) * cluster * kWarps) {
+    P.mode = kCluster;
+    P.cluster = cluster;
+    P.ctas = static_cast<int>(segments) * cluster;
+  } else {
+    P.mode = kLine;
+    const int64_t most = static_cast<int64_t>(kSms) * kWarps;
+    const int64_t workers = std::min(most, (segments * (steps + kSegmentCost) + kMinSteps - 1) / kMinSteps);
+    P.workers = static_cast<int>(workers);
+    P.ctas = static_cast<int>(std::min<int64_t>(kSms, workers));
     const size_t slots = 2 * static_cast<size_t>(workers) * 8 * P.nt;
     P.off_ml = slots * d * sizeof(float);
     P.bytes = (P.off_ml + slots * sizeof(float2) + 255) / 256 * 256;
@@ -1135,20 +1277,36 @@ Plan plan_of(int B, int H, int H_kv, int n_q, int d, int max_len, int format) {
   return P;
 }
 
-template <typename T, int D, int FMT, int NT, bool SPLIT>
+template <typename T, int D, int FMT, int NT, Mode MODE>
 cudaError_t launch_one(const DecodeParams& p, const Plan& P, cudaStream_t st) {
   using S = Step<D, FMT>;
   constexpr int kRing = kWarps * kStages * S::STAGE;
-  const size_t smem = kRing + (SPLIT ? (static_cast<size_t>(p.B) + 1) * sizeof(int) : 0);
-  auto* f = k_attn_decode<T, D, FMT, NT, SPLIT>;
+  const size_t smem = kRing + (MODE == kLine ? (static_cast<size_t>(p.B) + 1) * sizeof(int) + p.B : 0);
+  auto* f = k_attn_decode<T, D, FMT, NT, MODE>;
   static OncePerDevice once;
   cudaError_t e = once.run([&] {
-    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kRing + (SPLIT ? (kMaxBatch + 1) * static_cast<int>(sizeof(int)) : 0));
+    return cudaFuncSetAttribute(
+        f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        kRing + (MODE == kLine ? (kMaxBatch + 1) * static_cast<int>(sizeof(int)) + kMaxBatch : 0));
   });
   if (e != cudaSuccess) return e;
+  if (MODE == kCluster) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(P.ctas);
+    cfg.blockDim = dim3((kWarps + kFeeders) * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = P.cluster;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, f, p);
+  }
   f<<<P.ctas, (kWarps + kFeeders) * 32, smem, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess || !SPLIT) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess || MODE != kLine) return e;
   cudaLaunchConfig_t cfg = {};
   // A CTA takes all rows of a segment (with a CTA a row, 2048 rows of two to five
   // pieces took 9 us where this takes 4), and fewer where that leaves SMs idle.
@@ -1168,11 +1326,15 @@ cudaError_t launch_one(const DecodeParams& p, const Plan& P, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k_attn_join<T, D>, p, 8 * NT, per_cta, parts);
 }
 
+template <typename T, int D, int FMT, int NT>
+cudaError_t launch_nt(const DecodeParams& p, const Plan& P, cudaStream_t st) {
+  if (P.mode == kOne) return launch_one<T, D, FMT, NT, kOne>(p, P, st);
+  if (P.mode == kCluster) return launch_one<T, D, FMT, NT, kCluster>(p, P, st);
+  return launch_one<T, D, FMT, NT, kLine>(p, P, st);
+}
 template <typename T, int D, int FMT>
 cudaError_t launch_fmt(const DecodeParams& p, const Plan& P, cudaStream_t st) {
-  if (P.nt == 1)
-    return P.split ? launch_one<T, D, FMT, 1, true>(p, P, st) : launch_one<T, D, FMT, 1, false>(p, P, st);
-  return P.split ? launch_one<T, D, FMT, 2, true>(p, P, st) : launch_one<T, D, FMT, 2, false>(p, P, st);
+  return P.nt == 1 ? launch_nt<T, D, FMT, 1>(p, P, st) : launch_nt<T, D, FMT, 2>(p, P, st);
 }
 template <typename T, int D>
 cudaError_t launch_d(const DecodeParams& p, const Plan& P, int format, cudaStream_t st) {
@@ -1214,7 +1376,7 @@ cudaError_t launch_attn_decode(const DecodeArgs& a, cudaStream_t st) {
   p.lens = a.seq_lens;
   p.o = static_cast<uint8_t*>(a.o);
   p.lse = a.lse;
-  if (P.split) {
+  if (P.mode == kLine) {
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     p.part_o = reinterpret_cast<float*>(ws);
     p.part_ml = reinterpret_cast<float2*>(ws + P.off_ml);
@@ -1233,6 +1395,7 @@ cudaError_t launch_attn_decode(const DecodeArgs& a, cudaStream_t st) {
   p.causal = a.causal;
   p.workers = P.workers;
   p.step_tokens = P.step_tokens;
+  p.cluster = P.cluster;
   p.timeout_ns = a.timeout_ns;
   p.scale_log2 = a.sm_scale * 1.4426950408889634f;
   if (c.dtype == SAGE_F16)

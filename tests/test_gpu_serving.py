@@ -397,6 +397,24 @@ def test_decode_several_tokens(sage, dtype, fmt, d, nq, H, Hk, causal):
     check_decode(got, plain_decode(q, K, V, lens, causal, 0.2))
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("fmt", ["16", "B", "8+8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,H,Hk,P", [(1, 4, 4, 48), (1, 20, 4, 32), (5, 20, 4, 16)])
+def test_decode_batch_on_one_line(sage, dtype, fmt, d, nq, H, Hk, P):
+    """Requests enough that all segments share one line of steps; some empty,
+    some of one token, one much longer than the rest."""
+    r = np.random.default_rng(nq + P)
+    lens = [int(x) for x in r.integers(0, 300, 44)] + [0, 1, 2000, 0, 15, 16, 17]
+    c, table, K, V = filled_cache(sage, lens, Hk, P, d, fmt, dtype, seed=nq)
+    q = torch.randn(len(lens), H, nq, d, generator=gen(5), device="cuda").to(dtype)
+    assert sage.sage_attn_decode_workspace_bytes(len(lens), H, Hk, nq, d, 2000, fmt) > 0
+    got = sage.sage_attn_decode_paged(q, c, table, ints(lens), 2000, return_lse=True)
+    check_decode(got, plain_decode(q, K, V, lens, True, 1 / math.sqrt(d)))
+    again = sage.sage_attn_decode_paged(q, c, table, ints(lens), 2000, return_lse=True)
+    assert same_bits(got[0], again[0]) and same_bits(got[1], again[1])
+
+
 @pytest.mark.parametrize("B,n,Hk", [(200, 90, 4), (300, 700, 2), (3, 20000, 1), (1, 66000, 2)])
 def test_decode_many_and_long(sage, B, n, Hk):
     """Stretches of several segments, and segments of many stretches."""
@@ -487,11 +505,12 @@ def test_decode_two_graphs_share_a_workspace(sage):
     """Two captured calls of different sizes on one workspace, replayed in turn
     over a workspace full of NaN."""
     cases = []
-    for seed, lens in ((1, [2000, 17]), (2, [64, 900, 5, 0])):
+    for seed, lens in ((1, [40000, 17]), (2, [64, 33000, 5, 0])):
         c, table, K, V = filled_cache(sage, lens, 2, 16, 64, "B", torch.float16, seed=seed)
         q = torch.randn(len(lens), 6, 1, 64, generator=gen(seed), device="cuda").half()
         cases.append((q, c, table, ints(lens), max(lens), plain_decode(q, K, V, lens, True, 0.125)))
     need = max(sage.sage_attn_decode_workspace_bytes(q.shape[0], 6, 2, 1, 64, n, "B") for q, _, _, _, n, _ in cases)
+    assert need > 0
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     graphs = []
     for q, c, table, lens, n, _ in cases:

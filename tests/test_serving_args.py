@@ -78,9 +78,9 @@ def test_decode_refusals(lib):
     assert call(q=None) == 1 and call(s=None) == 1 and call(table=None) == 1 and call(lens=None) == 1 and call(o=None) == 1
     assert call(H=7) == 2 and call(B=4097) == 2 and call(nq=257) == 2
     assert call(q=ODD) == 3 and call(o=ODD) == 3 and call(lens=P(OK + 1)) == 3 and call(s=strides(1024, 132, 128)) == 3
-    assert call(ws=P(OK + 16)) == 3 and call(ws=None) == 1
-    need = lib.sage_attn_decode_workspace_bytes(3, 8, 2, 1, 128, 2000, 2)
-    assert need > 0 and call(bytes=need - 1) == 7
+    assert call(max_pages=1000, max_len=60000, ws=P(OK + 16)) == 3 and call(max_pages=1000, max_len=60000, ws=None) == 1
+    need = lib.sage_attn_decode_workspace_bytes(3, 8, 2, 1, 128, 60000, 2)
+    assert need > 0 and call(max_pages=1000, max_len=60000, bytes=need - 1) == 7
     assert call(B=0, q=None, lens=None, o=None) == 0 and call(nq=0, q=None, o=None) == 0
 
 
@@ -89,6 +89,7 @@ def test_decode_workspace_sizes(lib):
     assert f(0, 8, 2, 1, 128, 2000, 2) == 0 and f(3, 8, 2, 0, 128, 2000, 2) == 0
     assert f(3, 8, 3, 1, 128, 2000, 2) == 0 and f(3, 8, 2, 1, 96, 2000, 2) == 0 and f(3, 8, 2, 1, 128, 2000, 9) == 0
     assert f(4, 8, 2, 1, 128, 16, 0) == 0          # short caches are not split
+    assert f(4, 8, 2, 1, 128, 2000, 0) == 0        # nor are few longer ones, but within a cluster
     assert f(4096, 8, 2, 1, 128, 1 << 20, 0) < 1 << 27
 
 
