@@ -397,7 +397,8 @@ sage_status_t sage_rope_axes(const void* q, const int64_t* q_strides, void* q_ou
  *   K: delta = max|x| * (1 / 127), code = RNE(x / delta)
  *   V: delta = max|v| * (1 / 448), code = e4m3_rne_satfinite(v / delta)
  * (the constants, the products and the divisions each rounded to fp32), with
- * delta = 0 and codes 0 where delta would be below 2^-100.
+ * delta = 0 and codes 0 where delta would be below 2^-100; a zero of V of either
+ * sign has code 0.
  */
 sage_status_t sage_kv_append(const void* k, const int64_t* k_strides, const void* v,
                              const int64_t* v_strides, int T, const int32_t* slot_map,

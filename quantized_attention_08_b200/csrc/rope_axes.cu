@@ -23,7 +23,9 @@
 namespace sage {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 4;  // heads loaded before the first is rotated
+// Heads loaded before the first is rotated: 2 heads take 88 us on H 16 + 16, N
+// 32768, d 128, fp16 (537 MB: 0.93 of the measured copy rate), 1 97, 4 93.
+constexpr int kRopeUnroll = 2;
 
 template <typename T>
 __device__ __forceinline__ float2 rope_unpack(uint32_t w);

@@ -106,6 +106,30 @@ def test_slots(sage, B, P, T, free_n, top_ctx, top_new):
         assert np.array_equal(tt.cpu().numpy(), want[6])
 
 
+@pytest.mark.parametrize("B,T", [(3, 900), (700, 3000), (64, 64), (2000, 20000)])
+def test_slots_in_place(sage, B, T):
+    """seq_lens over ctx_lens and the free list's count over itself."""
+    r = np.random.default_rng(B)
+    ctx, new = r.integers(0, 60, B), r.integers(0, 2 * T // B, B)
+    P, width = 16, 200
+    held = [-(-int(c) // P) for c in ctx]
+    table = np.full((B, width), -7, np.int32)
+    ids = r.permutation(sum(held) + B + T).astype(np.int32)
+    at = 0
+    for b, n in enumerate(held):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    free = ids[at:]
+    want = plain_slots(ctx.tolist(), new.tolist(), free.tolist(), 1, table, P, T)
+    lens, used, tt = ints(ctx.tolist()), ints([1]), torch.from_numpy(table).cuda()
+    e = lambda n: torch.empty(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    got = sage.sage_kv_slots(lens, ints(new.tolist()), torch.from_numpy(free).cuda(), used, tt, page_size=P, T=T,
+                             out=(lens, e(B + 1), e(T), e(T), e(T), used))
+    for g, w in zip(got, want):
+        assert g.cpu().numpy().tolist() == np.atleast_1d(w).tolist()
+    assert np.array_equal(tt.cpu().numpy(), want[6])
+
+
 def test_slots_in_place_replayed(sage):
     """A captured decode step whose lengths and free list advance in place."""
     B, P, steps = 5, 16, 40
@@ -277,6 +301,7 @@ def test_append(sage, dtype, fmt, d, T, Hk, P, mean):
     if fmt == "8+8":
         delta, y = plain_codes(w, 448)
         assert same_bits(rows(c.v_scale), delta.float())
+        y = torch.where(w == 0, torch.zeros_like(y), y)  # a zero of either sign is code 0
         assert same_bits(rows(c.v), y.float().to(torch.float8_e4m3fn).view(torch.uint8))
     else:
         assert same_bits(rows(c.v), v[:, live])
