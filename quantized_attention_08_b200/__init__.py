@@ -577,8 +577,8 @@ def sage_kv_slots(ctx_lens, new_lens, free_pages, free_used, block_table, *, pag
     i32, dev = torch.int32, ctx_lens.get_device()
     B, F, width = ctx_lens.numel(), free_pages.numel(), block_table.shape[-1]
     if out is None:
-        if T < 0:
-            raise ValueError("T must not be negative")
+        if T < 0 or page_size > 0x7fffffff:
+            raise ValueError(f"T must not be negative, nor page_size past 2^31: got {T}, {page_size}")
         out = torch.empty(2 * B + 3 * T + 2, dtype=i32, device=ctx_lens.device).split_with_sizes(
             (B, B + 1, T, T, T, 1))
         lens = out[0].data_ptr()
@@ -728,6 +728,8 @@ def sage_attn_decode_paged(q, cache: SageKVCache, block_table, seq_lens, max_len
     else:
         raise ValueError(f"q must be [B, H, n_q, {d}] or [B, H, {d}]")
     width = block_table.shape[-1]
+    if max_len > 0x7fffffff:  # would wrap around in the C call
+        raise ValueError(f"max_len must be below 2^31, got {max_len}")
     if o is None:
         o = torch.empty_like(q, memory_format=torch.contiguous_format)
         op = o.data_ptr()

@@ -465,18 +465,16 @@ __device__ __forceinline__ void feed(const DecodeParams& p, const Requests& q, u
       __nanosleep(20);
     }
   }
-  if (__any_sync(0xffffffffu, *abort_flag != 0)) {
-    // Given up.  The copies under way write to this CTA's memory: wait for
-    // them, as long again at most.
-    since = globaltimer();
-    while (issued-- > 0) {
-      if (--slot < 0) {
-        slot = kStages - 1;
-        parity ^= 1;
-      }
-      while (!mbar_test_wait(full + slot, parity) && globaltimer() - since < p.timeout_ns) {
-      }
+  // The copies under way write to this CTA's memory: stay until they have landed,
+  // also where a consumer has given up (as long again at most, and 10 ms at least).
+  since = globaltimer();
+  const uint64_t limit = p.timeout_ns > 10000000 ? p.timeout_ns : 10000000;
+  while (issued-- > 0) {
+    if (--slot < 0) {
+      slot = kStages - 1;
+      parity ^= 1;
     }
+    while (!mbar_test_wait(full + slot, parity) && globaltimer() - since < limit) __nanosleep(100);
   }
 }
 
@@ -497,6 +495,7 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t a, int rank) {
 template <typename T, int D, int ROWS>
 __device__ __forceinline__ void join_cluster(const DecodeParams& p, int b, int h, int row0, int steps, uint8_t* smem,
                                              int ring_bytes) {
+  __syncwarp();
   cluster_barrier();
   const int rows = min(ROWS, p.rows - row0);
   const int per = cluster_steps(steps, p.cluster);
@@ -554,6 +553,7 @@ __device__ __forceinline__ void join_cluster(const DecodeParams& p, int b, int h
         p.lse[out] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
   }
+  __syncwarp();
   cluster_barrier();  // no CTA leaves while another reads its memory
 }
 

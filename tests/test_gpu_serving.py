@@ -451,6 +451,74 @@ def test_decode_many_and_long(sage, B, n, Hk):
     check_decode(got, plain_decode(q, K, V, lens, True, 0.125))
 
 
+def test_decode_largest_batch(sage):
+    """4096 requests, the most a call takes, and the most shared memory."""
+    lens = [int(x) for x in np.random.default_rng(3).integers(0, 200, 4095)] + [700]
+    c, table, K, V = filled_cache(sage, lens, 1, 16, 64, "8+8", torch.float16, seed=12)
+    q = torch.randn(4096, 2, 64, generator=gen(6), device="cuda").half()
+    o, lse = sage.sage_attn_decode_paged(q, c, table, ints(lens), 700, return_lse=True)
+    some = list(range(0, 4096, 97)) + [4095]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    keep = torch.cat([torch.arange(cu[b], cu[b + 1]) for b in some]).cuda()
+    want = plain_decode(q[some][:, :, None], K[:, keep], V[:, keep], [lens[b] for b in some], True, 0.125)
+    check_decode((o[some][:, :, None], lse[some][:, :, None]), want)
+    empty = torch.tensor([n == 0 for n in lens], device="cuda")
+    assert bool((o[empty] == 0).all()) and bool(torch.isneginf(lse[empty]).all())
+
+
+def test_decode_two_streams_at_once(sage):
+    """Two calls that may overlap, each with its own stream and workspace."""
+    cases = []
+    for seed, fmt, lens in ((1, "8+8", [30000, 200, 0, 5]), (2, "16", [9, 20000])):
+        c, table, K, V = filled_cache(sage, lens, 4, 32, 128, fmt, torch.bfloat16, seed=seed)
+        q = torch.randn(len(lens), 8, 1, 128, generator=gen(seed), device="cuda").bfloat16()
+        cases.append((q, c, table, ints(lens), max(lens), plain_decode(q, K, V, lens, True, 128 ** -0.5)))
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        for s, (q, c, table, lens, n, _w) in zip(streams, cases):
+            outs.append(sage.sage_attn_decode_paged(q, c, table, lens, n, return_lse=True, stream=s))
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        check_decode(o, cases[i % 2][5])
+        assert same_bits(o[0], outs[i % 2][0])
+
+
+def test_decode_growing_request_in_one_graph(sage):
+    """One captured call, replayed while the request grows across steps, pages,
+    and from one warp's work to many; stale NaN stands behind the last token."""
+    n, P, d = 700, 16, 64
+    c, table, K, V = filled_cache(sage, [n], 2, P, d, "16", torch.float16, seed=4)
+    q = torch.randn(1, 4, 1, d, generator=gen(2), device="cuda").half()
+    lens = ints([1])
+    run = lambda: sage.sage_attn_decode_paged(q, c, table, lens, n, return_lse=True)  # noqa: E731
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run()
+    for m in (0, 1, 2, 15, 16, 17, 31, 32, 33, 64, 255, 256, 257, 512, 699, 700):
+        lens.fill_(m)
+        g.replay()
+        torch.cuda.synchronize()
+        check_decode(out, plain_decode(q, K[:, :m], V[:, :m], [m], True, 0.125))
+
+
+def test_decode_small_v_beside_large(sage):
+    """Rows of V whose scales differ by 2^12: the unit that P is taken in grows in
+    the middle of a request."""
+    d, n = 128, 400
+    c, table, K, V = filled_cache(sage, [n], 1, 16, d, "8+8", torch.bfloat16, seed=6)
+    at = torch.arange(0, n // 2, device="cuda")
+    pg, off = table[0, at // 16].long(), at % 16
+    c.v_scale[pg, 0, off] *= 2.0 ** -12
+    V[:, :n // 2] *= 2.0 ** -12
+    q = torch.randn(1, 3, 1, d, generator=gen(2), device="cuda").bfloat16()
+    got = sage.sage_attn_decode_paged(q, c, table, ints([n]), n, return_lse=True)
+    check_decode(got, plain_decode(q, K, V, [n], True, d ** -0.5))
+
+
 def test_decode_extremes(sage):
     """A score far above the rest at either end, equal scores, and small and
     large V (fp16 rows near its smallest and largest numbers)."""

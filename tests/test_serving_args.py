@@ -155,6 +155,8 @@ def test_binding_refusals():
         sage.sage_kv_slots(i(3), i(3), i(9), i(1), i(4, 3).t(), page_size=16, T=3)
     with pytest.raises(ValueError):
         sage.sage_kv_slots(i(3), i(3), i(9), i(1), i(3, 4), page_size=16, T=-1)
+    with pytest.raises(ValueError):
+        sage.sage_kv_slots(i(3), i(3), i(9), i(1), i(3, 4), page_size=1 << 32, T=1)
     f = torch.zeros(32)
     with pytest.raises(TypeError):
         sage.sage_rope_axes(h(1, 2, 5, 64).float(), None, i(1, 5), f, [32])
