@@ -21,7 +21,6 @@ Serving from a paged key-value cache (SageKVCache holds one; fp16 and bf16):
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 from typing import Optional
@@ -30,6 +29,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsage.so")
+SERVING_PATH = os.path.join(_PKG, "_serving.so")
 
 SAGE_OK = 0
 SAGE_ERR_DEVICE_TIMEOUT = 6
@@ -422,9 +422,6 @@ def sage_attn_fwd_varlen(q, k, v, cu_seqlens, max_seqlen: int, *, causal: bool =
 # ------------------------------------------------- serving from a paged cache
 KV_FORMATS = {"16": 0, "B": 1, "8+8": 2}
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
-_i64x3 = _c.c_int64 * 3
-_i64x4 = _c.c_int64 * 4
-_i64x14 = _c.c_int64 * 14
 
 
 class _CacheStruct(_c.Structure):
@@ -435,54 +432,34 @@ class _CacheStruct(_c.Structure):
                 ("dtype", _i)]
 
 
-# The serving calls of a decode step take microseconds on the GPU, so their
-# checks keep to cheap accessors: device numbers for devices, torch's raw
-# stream lookup, each library function looked up once, and outputs made like a
-# tensor that exists (a third of torch.empty's time).
-def _strided(t: torch.Tensor, dtype, name: str, dev: int):
-    """Checks of a strided argument (type, device number, last axis dense);
-    returns its strides."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
-    st = t.stride()
-    if not st or st[-1] != 1:
-        raise ValueError(f"{name} must be dense along its last axis")
-    return st
+# The serving calls of a decode step take microseconds on the GPU: their
+# arguments are checked and passed on by a small extension module
+# (csrc/serving_binding.cpp), which calls the same C functions.
+_ext_handle = None
 
 
-def _dense(t: torch.Tensor, dtype, name: str, dev: int, shape) -> int:
-    """Checks of a contiguous argument (type, device number, shape); returns
-    its address."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+def _ext():
+    """The extension module, with the library's functions (raises if it has not
+    been built)."""
+    global _ext_handle
+    if _ext_handle is None:
+        lib = load_library()
+        if not os.path.exists(SERVING_PATH):
+            raise RuntimeError(
+                f"{SERVING_PATH} is missing: build it first (python -m quantized_attention_08_b200.build)")
+        from . import _serving
+        _serving.bind(*(_c.cast(getattr(lib, name), _vp).value for name in (
+            "sage_kv_slots", "sage_rope_axes", "sage_kv_append", "sage_attn_decode_paged",
+            "sage_attn_decode_workspace_bytes")))
+        _ext_handle = _serving
+    return _ext_handle
 
 
-_fns = {}
-
-
-def _call(name: str, dev: int, *args):
-    """Calls the library with device `dev` current, on its current stream."""
-    if dev < 0:
-        raise TypeError(f"{name} takes CUDA tensors")
-    fn = _fns.get(name)
-    if fn is None:
-        fn = _fns[name] = getattr(load_library(), name)
-    if torch._C._cuda_getDevice() == dev:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    if status:
-        raise SageError(status, name)
+def _result(r, where: str):
+    """What an extension call returned: its outputs, or a status to raise."""
+    if r.__class__ is int:
+        _check(r, where)
+    return r
 
 
 def _with_stream(f, stream, t, *args, **kw):
@@ -574,27 +551,8 @@ def sage_kv_slots(ctx_lens, new_lens, free_pages, free_used, block_table, *, pag
     if stream is not None:
         return _with_stream(sage_kv_slots, stream, ctx_lens, new_lens, free_pages, free_used, block_table,
                             page_size=page_size, T=T, out=out)
-    i32, dev = torch.int32, ctx_lens.get_device()
-    B, F, width = ctx_lens.numel(), free_pages.numel(), block_table.shape[-1]
-    if out is None:
-        if T < 0 or page_size > 0x7fffffff:
-            raise ValueError(f"T must not be negative, nor page_size past 2^31: got {T}, {page_size}")
-        out = torch.empty(2 * B + 3 * T + 2, dtype=i32, device=ctx_lens.device).split_with_sizes(
-            (B, B + 1, T, T, T, 1))
-        lens = out[0].data_ptr()
-        cu = lens + 4 * B
-        slots = cu + 4 * B + 4
-        pos, ids, used = slots + 4 * T, slots + 8 * T, slots + 12 * T
-    else:
-        lens, cu, slots, pos, ids, used = (
-            _dense(t, i32, name, dev, (n,)) for t, name, n in
-            zip(out, ("seq_lens", "cu_seqlens", "slot_map", "positions", "seq_ids", "free_used"),
-                (B, B + 1, T, T, T, 1)))
-    _call("sage_kv_slots", dev, _dense(ctx_lens, i32, "ctx_lens", dev, (B,)),
-          _dense(new_lens, i32, "new_lens", dev, (B,)), B, _dense(free_pages, i32, "free_pages", dev, (F,)), F,
-          _dense(free_used, i32, "free_used", dev, (1,)),
-          _dense(block_table, i32, "block_table", dev, (B, width)), width, page_size, lens, cu, slots, pos, ids, T, used)
-    return out
+    return _result((_ext_handle or _ext()).kv_slots(ctx_lens, new_lens, free_pages, free_used, block_table, page_size,
+                                                    T, out), "sage_kv_slots")
 
 
 def sage_rope_axes(q, k, positions, inv_freq, sections, *, pairing: str = "half", q_out=None, k_out=None,
@@ -609,61 +567,10 @@ def sage_rope_axes(q, k, positions, inv_freq, sections, *, pairing: str = "half"
     if stream is not None:
         return _with_stream(sage_rope_axes, stream, q, k, positions, inv_freq, sections, pairing=pairing, q_out=q_out,
                             k_out=k_out)
-    dtype, dev, shape = q.dtype, q.get_device(), q.shape
-    code = _DTYPES.get(dtype)
-    if code is None:
-        raise TypeError(f"q must be torch.float16 or torch.bfloat16, got {dtype}")
     if pairing != "half" and pairing != "interleaved":
         raise ValueError(f"pairing must be 'half' or 'interleaved', got {pairing!r}")
-    if len(shape) == 4:
-        B, H, N, d = shape
-    elif len(shape) == 3:
-        B, (H, N, d) = 1, shape
-    else:
-        raise ValueError("q must be [B, H, N, d] or [H, N, d]")
-
-    # strides of q, q_out, k, k_out (batch, head, token) and positions, in one array
-    lead = () if len(shape) == 4 else (0,)
-    if q_out is None:
-        q_out = torch.empty_like(q)
-    elif q_out.shape != shape:
-        raise ValueError("q_out does not have the shape of its input")
-    st = (*lead, *_strided(q, dtype, "q", dev)[:-1], *lead, *_strided(q_out, dtype, "q_out", dev)[:-1])
-    if k is not None:
-        kshape = k.shape
-        if len(kshape) != len(shape) or kshape[-2:] != shape[-2:] or (not lead and kshape[0] != B):
-            raise ValueError("q and k must have the same batch, tokens and channels")
-        if k_out is None:
-            k_out = torch.empty_like(k)
-        elif k_out.shape != kshape:
-            raise ValueError("k_out does not have the shape of its input")
-        st += (*lead, *_strided(k, dtype, "k", dev)[:-1], *lead, *_strided(k_out, dtype, "k_out", dev)[:-1])
-        Hk, kp, kop = kshape[-3], k.data_ptr(), k_out.data_ptr()
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    else:
-        Hk, kp, kop = 0, None, None
-        st += (0,) * 6
-    A = len(sections)
-    ps = _strided(positions, torch.int32, "positions", dev)
-    pshape = positions.shape
-    if pshape == (A, B, N):
-        st += ps[:2]
-    elif pshape == (A, N):
-        st += (ps[0], 0)
-    else:
-        raise ValueError(f"positions must be [{A}, {N}] or [{A}, {B}, {N}], got {tuple(pshape)}")
-    inv = _dense(inv_freq, torch.float32, "inv_freq", dev, (sum(sections),))
-    arr = _i64x14(*st)
-    at = _c.addressof(arr)
-    _call("sage_rope_axes", dev, q.data_ptr(), at, q_out.data_ptr(), at + 24, kp, at + 48, kop, at + 72,
-          positions.data_ptr(), at + 96, inv, _axes(tuple(sections)), A, B, H, Hk, N, d, pairing != "half", code)
-    return q_out, k_out
-
-
-@functools.lru_cache(maxsize=64)
-def _axes(sections):
-    return (_i * len(sections))(*sections)
+    return _result((_ext_handle or _ext()).rope_axes(q, k, positions, inv_freq, sections, pairing != "half", q_out,
+                                                     k_out), "sage_rope_axes")
 
 
 def sage_kv_append(k, v, slot_map, cache: SageKVCache, *, mean_k=None, seq_ids=None, stream=None):
@@ -673,22 +580,8 @@ def sage_kv_append(k, v, slot_map, cache: SageKVCache, *, mean_k=None, seq_ids=N
     from K (Smooth K per request; every token of a request needs the same)."""
     if stream is not None:
         return _with_stream(sage_kv_append, stream, k, v, slot_map, cache, mean_k=mean_k, seq_ids=seq_ids)
-    dev, shape = cache._dev, k.shape
-    ks, vs = _strided(k, cache.dtype, "k", dev), _strided(v, cache.dtype, "v", dev)
-    if len(shape) != 3 or v.shape != shape or shape[0] != cache.H_kv or shape[2] != cache.d:
-        raise ValueError(f"k and v must both be [{cache.H_kv}, T, {cache.d}]")
-    T = shape[1]
-    B, mean, ids = 0, None, None
-    if mean_k is not None:
-        if seq_ids is None:
-            raise ValueError("mean_k needs seq_ids")
-        B = mean_k.shape[0]
-        mean = _dense(mean_k, torch.float32, "mean_k", dev, (B, cache.H_kv, cache.d))
-        ids = _dense(seq_ids, torch.int32, "seq_ids", dev, (T,))
-    arr = _i64x4(ks[0], ks[1], vs[0], vs[1])
-    at = _c.addressof(arr)
-    _call("sage_kv_append", dev, k.data_ptr(), at, v.data_ptr(), at + 16, T,
-          _dense(slot_map, torch.int32, "slot_map", dev, (T,)), mean, ids, B, cache._ref)
+    _result((_ext_handle or _ext()).kv_append(k, v, slot_map, cache._ref, cache._dev, mean_k, seq_ids),
+            "sage_kv_append")
     return cache
 
 
@@ -696,11 +589,6 @@ def sage_attn_decode_workspace_bytes(B: int, H: int, H_kv: int, n_q: int, d: int
                                      format="8+8") -> int:
     return load_library().sage_attn_decode_workspace_bytes(
         B, H, H_kv, n_q, d, max_len, KV_FORMATS[format] if isinstance(format, str) else int(format))
-
-
-@functools.lru_cache(maxsize=1024)
-def _decode_workspace(*sizes) -> int:
-    return load_library().sage_attn_decode_workspace_bytes(*sizes)
 
 
 def sage_attn_decode_paged(q, cache: SageKVCache, block_table, seq_lens, max_len: int, *,
@@ -716,44 +604,9 @@ def sage_attn_decode_paged(q, cache: SageKVCache, block_table, seq_lens, max_len
     if stream is not None:
         return _with_stream(sage_attn_decode_paged, stream, q, cache, block_table, seq_lens, max_len, causal=causal,
                             sm_scale=sm_scale, o=o, return_lse=return_lse, workspace=workspace)
-    dev, d, shape = cache._dev, cache.d, q.shape
-    qs = _strided(q, cache.dtype, "q", dev)
-    if len(shape) == 4 and shape[3] == d:
-        B, H, n_q, _ = shape
-        arr = _i64x3(qs[0], qs[1], qs[2])
-    elif len(shape) == 3 and shape[2] == d:
-        B, H, _ = shape
-        n_q = 1
-        arr = _i64x3(qs[0], qs[1], 0)
-    else:
-        raise ValueError(f"q must be [B, H, n_q, {d}] or [B, H, {d}]")
-    width = block_table.shape[-1]
-    if max_len > 0x7fffffff:  # would wrap around in the C call
-        raise ValueError(f"max_len must be below 2^31, got {max_len}")
-    if o is None:
-        o = torch.empty_like(q, memory_format=torch.contiguous_format)
-        op = o.data_ptr()
-    else:
-        op = _dense(o, q.dtype, "o", dev, shape)
-    lse, lp = None, None
-    if return_lse:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
-        lp = lse.data_ptr()
-    if workspace is None:
-        size = _decode_workspace(B, H, cache.H_kv, n_q, d, max_len, cache._struct.format)
-        ws = None
-        if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-            ws = workspace.data_ptr()
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
-    else:
-        ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call("sage_attn_decode_paged", dev, q.data_ptr(), arr, cache._ref,
-          _dense(block_table, torch.int32, "block_table", dev, (B, width)), width,
-          _dense(seq_lens, torch.int32, "seq_lens", dev, (B,)), B, H, n_q, max_len, 1 if causal else 0,
-          1.0 / math.sqrt(d) if sm_scale is None else sm_scale, op, lp, ws, size)
-    return (o, lse) if return_lse else o
+    return _result((_ext_handle or _ext()).attn_decode(q, cache._ref, cache._dev, block_table, seq_lens, max_len,
+                                                       causal, sm_scale, o, return_lse, workspace),
+                   "sage_attn_decode_paged")
 
 
 def sage_get_device_error(stream=None):
