@@ -68,11 +68,13 @@ enum Mode {
 };
 constexpr int kMaxCluster = 8;      // portable
 // A cluster a segment saves a launch and the workspace; it pays while a warp has
-// no more steps than this and all clusters find room at once (16 clusters of 8
-// did not: 19 us where the line takes 10).  One request, 8 kv heads, 16 bits:
-// 500 tokens 6.5 us against 8.2, 1009 8.6 against 8.9, 2048 10.1 against 9.2
-// (and a launch less on the host), 8192 17.8 against 14.0.
-constexpr int kClusterSteps = 2;
+// no more than four steps (two where its CTAs would leave most SMs idle), and
+// only while all clusters find room at once (16 clusters of 8 did not: 19 us where
+// the line takes 10).  8 kv heads, 16 bits, device time against the line's: one
+// request of 1009 tokens 6.0 us, 8.5; 4096 10.5, 11.4; 8192 15.4, 14.0; four
+// requests of 2048 10.5, 12.9.  One kv head, 2048 tokens: 8.3, 7.1 (a launch less on
+// the host); 4096: 11.3, 7.7.
+constexpr int kClusterSteps = 4, kClusterStepsFew = 2, kClusterFew = 32;
 constexpr int kClusterCtas = 128, kCluster8Ctas = 64;
 // What beginning a segment costs, in steps: the line counts each segment as that
 // much longer, so that a warp with many short ones gets fewer steps.
@@ -478,9 +480,10 @@ __device__ __forceinline__ void feed(const DecodeParams& p, const Requests& q, u
   }
 }
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // the address of this CTA's shared address `a` in CTA `rank` of the cluster
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t a, int rank) {
   uint32_t r;
@@ -488,73 +491,95 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t a, int rank) {
   return r;
 }
 
-// Joins the pieces that the consuming warps of a cluster have left in their rings
-// (O [ROWS][D] and (m, l) [ROWS] each; the first warps hold all the steps).
-// Sixteen lanes share four channels of a row, each of them a sixteenth of the
-// pieces; the CTAs of the cluster take turns at the channels.
-template <typename T, int D, int ROWS>
-__device__ __forceinline__ void join_cluster(const DecodeParams& p, int b, int h, int row0, int steps, uint8_t* smem,
-                                             int ring_bytes) {
-  __syncwarp();
-  cluster_barrier();
-  const int rows = min(ROWS, p.rows - row0);
-  const int per = cluster_steps(steps, p.cluster);
-  const int pieces = steps > 0 ? (steps + per - 1) / per : 0;
-  const uint32_t base = smem_u32(smem);
-  const int sub = threadIdx.x & 15;
-  const int rank = blockIdx.x % p.cluster;
-  const int units = rows * (D / 4);  // of four channels
-  for (int u0 = rank; u0 < units; u0 += p.cluster * (kWarps * 2)) {
-    const int u = u0 + (threadIdx.x >> 4) * p.cluster;
-    const bool in = u < units;
-    const int r = in ? u / (D / 4) : 0, ch = in ? (u - r * (D / 4)) * 4 : 0;
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    constexpr int kMost = kMaxCluster * kWarps / 16;  // pieces of a lane
-    float ml[kMost][2], x[kMost][4];
+// pieces of four channels of a row, joined: o (in units of 2^m) and l
+struct Four {
+  float o[4], m, l;
+};
+// `n` pieces, piece i's (m, l) and O at the addresses that `ml` and `o` give
+template <typename ML, typename O>
+__device__ __forceinline__ Four join_four(int n, ML ml, O o) {
+  Four r = {{0.f, 0.f, 0.f, 0.f}, -INFINITY, 0.f};
+  float2 w[kWarps];
+  float4 x[kWarps];
 #pragma unroll
-    for (int j = 0; j < kMost; ++j) {
-      const int i = sub + 16 * j;
-      ml[j][0] = -INFINITY;
-      ml[j][1] = x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
-      if (in && i < pieces) {
-        const int w = i / p.cluster;
-        const uint32_t a = cluster_addr(base + w * ring_bytes, i - w * p.cluster);
-        asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
-                     : "=f"(ml[j][0]), "=f"(ml[j][1])
-                     : "r"(a + ROWS * D * 4 + r * 8));
-        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(x[j][0]), "=f"(x[j][1]), "=f"(x[j][2]), "=f"(x[j][3])
-                     : "r"(a + (r * D + ch) * 4));
-      }
-      m = fmaxf(m, ml[j][0]);
+  for (int i = 0; i < kWarps; ++i) {
+    w[i] = make_float2(-INFINITY, 0.f);
+    if (i < n) {
+      w[i] = *ml(i);
+      x[i] = *o(i);
     }
+    r.m = fmaxf(r.m, w[i].x);
+  }
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-#pragma unroll
-    for (int j = 0; j < kMost; ++j) {
-      const float f = ml[j][0] == -INFINITY ? 0.f : exp2_fast(ml[j][0] - m);
-      l += ml[j][1] * f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] += x[j][e] * f;
-    }
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, d);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] += __shfl_xor_sync(0xffffffffu, o[e], d);
-    }
-    if (in && sub == 0) {
-      const int row = row0 + r, qi = row / p.G;
-      const int64_t out = (static_cast<int64_t>(b) * p.H + h * p.G + (row - qi * p.G)) * p.n_q + qi;
-      const float f = l > 0.f ? 1.f / l : 0.f;
-      *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.o) + out * D + ch) =
-          make_uint2(pack16<T>(o[0] * f, o[1] * f), pack16<T>(o[2] * f, o[3] * f));
-      if (p.lse != nullptr && ch == 0)
-        p.lse[out] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < n && w[i].x != -INFINITY) {
+      const float f = exp2_fast(w[i].x - r.m);
+      r.l += w[i].y * f;
+      r.o[0] += x[i].x * f;
+      r.o[1] += x[i].y * f;
+      r.o[2] += x[i].z * f;
+      r.o[3] += x[i].w * f;
     }
   }
+  return r;
+}
+
+// Bytes of a cluster CTA's inbox: (m, l) and O of four channels of every row.
+template <int D, int ROWS>
+constexpr int inbox_bytes() {
+  return ROWS * (D / 4) * 24;
+}
+
+// Joins the pieces that the consuming warps of a cluster have left in their rings
+// (O [ROWS][D] and (m, l) [ROWS] each).  Each CTA joins its own eight, then sends
+// every unit of four channels to the CTA that writes it (remote stores: nobody
+// waits for them but the barrier), which joins what the CTAs sent.  Reading the 64
+// pieces of a cluster remotely took 3 us where this takes 1.
+template <typename T, int D, int ROWS>
+__device__ __forceinline__ void join_cluster(const DecodeParams& p, int b, int h, int row0, uint8_t* smem,
+                                             int ring_bytes) {
+  static_assert(kMaxCluster <= kWarps, "join_four takes kWarps pieces");
   __syncwarp();
-  cluster_barrier();  // no CTA leaves while another reads its memory
+  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+  const int rows = min(ROWS, p.rows - row0);
+  const int units = rows * (D / 4);
+  const int rank = blockIdx.x % p.cluster;
+  // the inbox behind the rings: float4 [unit / cluster][source], then float2 alike
+  uint8_t* const box = smem + kWarps * ring_bytes;
+  const int places = (units + p.cluster - 1) / p.cluster * p.cluster;
+  cluster_wait();  // of the kernel's beginning: every CTA is there
+  for (int u = threadIdx.x; u < units; u += kWarps * 32) {
+    const int r = u / (D / 4), ch = (u - r * (D / 4)) * 4;
+    const Four f = join_four(
+        kWarps,
+        [&](int i) { return reinterpret_cast<const float2*>(smem + i * ring_bytes + ROWS * D * 4) + r; },
+        [&](int i) { return reinterpret_cast<const float4*>(smem + i * ring_bytes + (r * D + ch) * 4); });
+    const int place = u / p.cluster, to = u - place * p.cluster;
+    const uint32_t a = cluster_addr(smem_u32(box) + (place * p.cluster + rank) * 16, to);
+    const uint32_t c = cluster_addr(smem_u32(box) + places * 16 + (place * p.cluster + rank) * 8, to);
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(f.o[0]), "f"(f.o[1]), "f"(f.o[2]),
+                 "f"(f.o[3])
+                 : "memory");
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(c), "f"(f.m), "f"(f.l) : "memory");
+  }
+  __syncwarp();
+  cluster_arrive();
+  cluster_wait();
+  for (int place = threadIdx.x; place * p.cluster + rank < units; place += kWarps * 32) {
+    const int u = place * p.cluster + rank;
+    const int r = u / (D / 4), ch = (u - r * (D / 4)) * 4;
+    const Four f = join_four(
+        p.cluster,
+        [&](int i) { return reinterpret_cast<const float2*>(box + places * 16) + place * p.cluster + i; },
+        [&](int i) { return reinterpret_cast<const float4*>(box) + place * p.cluster + i; });
+    const int row = row0 + r, qi = row / p.G;
+    const int64_t out = (static_cast<int64_t>(b) * p.H + h * p.G + (row - qi * p.G)) * p.n_q + qi;
+    const float g = f.l > 0.f ? 1.f / f.l : 0.f;
+    *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.o) + out * D + ch) =
+        make_uint2(pack16<T>(f.o[0] * g, f.o[1] * g), pack16<T>(f.o[2] * g, f.o[3] * g));
+    if (p.lse != nullptr && ch == 0)
+      p.lse[out] = f.l > 0.f ? (f.m + log2f(f.l)) * 0.69314718055994531f : -INFINITY;
+  }
 }
 
 template <typename T, int D, int FMT, int NT, Mode MODE>
@@ -581,6 +606,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
     fence_mbar_init();
   }
   if (threadIdx.x == 0) s_abort = 0;
+  if (MODE == kCluster) cluster_arrive();  // before the first remote store, all CTAs have started
   if (MODE == kLine) {
     // the join's CTAs may be placed now; they wait for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1017,7 +1043,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
         }
       }
     if (MODE == kCluster) {
-      join_cluster<T, D, ROWS>(p, cur.b, h, row0, cur.steps, smem, kStages * S::STAGE);
+      join_cluster<T, D, ROWS>(p, cur.b, h, row0, smem, kStages * S::STAGE);
       return;
     }
     first_piece = false;
@@ -1260,7 +1286,8 @@ Plan plan_of(int B, int H, int H_kv, int n_q, int d, int max_len, int format) {
     P.mode = kOne;
     P.workers = static_cast<int>(segments);
     P.ctas = static_cast<int>(std::max<int64_t>(std::min<int64_t>(kSms, segments), (segments + kWarps - 1) / kWarps));
-  } else if (cluster > 1 && steps <= static_cast<int64_t>(kClusterSteps) * cluster * kWarps) {
+  } else if (cluster > 1 && steps <= (segments * cluster < kClusterFew ? kClusterStepsFew : kClusterSteps) *
+                                         static_cast<int64_t>(cluster) * kWarps) {
     P.mode = kCluster;
     P.cluster = cluster;
     P.ctas = static_cast<int>(segments) * cluster;
@@ -1281,13 +1308,14 @@ template <typename T, int D, int FMT, int NT, Mode MODE>
 cudaError_t launch_one(const DecodeParams& p, const Plan& P, cudaStream_t st) {
   using S = Step<D, FMT>;
   constexpr int kRing = kWarps * kStages * S::STAGE;
-  const size_t smem = kRing + (MODE == kLine ? (static_cast<size_t>(p.B) + 1) * sizeof(int) + p.B : 0);
+  constexpr int kInbox = MODE == kCluster ? inbox_bytes<D, 8 * NT>() : 0;
+  const size_t smem = kRing + kInbox + (MODE == kLine ? (static_cast<size_t>(p.B) + 1) * sizeof(int) + p.B : 0);
   auto* f = k_attn_decode<T, D, FMT, NT, MODE>;
   static OncePerDevice once;
   cudaError_t e = once.run([&] {
     return cudaFuncSetAttribute(
         f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        kRing + (MODE == kLine ? (kMaxBatch + 1) * static_cast<int>(sizeof(int)) + kMaxBatch : 0));
+        kRing + kInbox + (MODE == kLine ? (kMaxBatch + 1) * static_cast<int>(sizeof(int)) + kMaxBatch : 0));
   });
   if (e != cudaSuccess) return e;
   if (MODE == kCluster) {
