@@ -606,6 +606,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
     fence_mbar_init();
   }
   if (threadIdx.x == 0) s_abort = 0;
+  after_previous();  // and before the join may be placed: it reads the lengths while this grid runs
   if (MODE == kCluster) cluster_arrive();  // before the first remote store, all CTAs have started
   if (MODE == kLine) {
     // the join's CTAs may be placed now; they wait for this grid's end
@@ -1134,7 +1135,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const DecodeParam
     all += s_steps[w].y;
   }
   const int places = places_of(clamp_len(p, p.lens[b]), p.step_tokens);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
   if (places == 0) {
     for (int rg = first + warp; rg < last; rg += kJoinWarps) {
       const int64_t out = out_of(rg);
@@ -1318,24 +1319,9 @@ cudaError_t launch_one(const DecodeParams& p, const Plan& P, cudaStream_t st) {
         kRing + kInbox + (MODE == kLine ? (kMaxBatch + 1) * static_cast<int>(sizeof(int)) + kMaxBatch : 0));
   });
   if (e != cudaSuccess) return e;
-  if (MODE == kCluster) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(P.ctas);
-    cfg.blockDim = dim3((kWarps + kFeeders) * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = P.cluster;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, f, p);
-  }
-  f<<<P.ctas, (kWarps + kFeeders) * 32, smem, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess || MODE != kLine) return e;
-  cudaLaunchConfig_t cfg = {};
+  if (MODE == kCluster) return launch_after(f, dim3(P.ctas), (kWarps + kFeeders) * 32, smem, st, P.cluster, p);
+  e = launch_after(f, dim3(P.ctas), (kWarps + kFeeders) * 32, smem, st, 1, p);
+  if (e != cudaSuccess || MODE != kLine) return e;
   // A CTA takes all rows of a segment (with a CTA a row, 2048 rows of two to five
   // pieces took 9 us where this takes 4), and fewer where that leaves SMs idle.
   const int in_group = std::min(8 * NT, p.rows);
@@ -1343,17 +1329,9 @@ cudaError_t launch_one(const DecodeParams& p, const Plan& P, cudaStream_t st) {
   int per_cta = in_group;
   while (per_cta > 1 && segments * ((in_group + per_cta - 1) / per_cta) < 2 * kSms) per_cta = (per_cta + 1) / 2;
   const int parts = (in_group + per_cta - 1) / per_cta;
-  cfg.gridDim = dim3(parts * p.groups * p.Hk, p.B);
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_attn_join<T, D>, p, 8 * NT, per_cta, parts);
+  return launch_after(k_attn_join<T, D>, dim3(parts * p.groups * p.Hk, p.B), kJoinWarps * 32, 0, st, 1, p, 8 * NT,
+                      per_cta, parts);
 }
-
 template <typename T, int D, int FMT, int NT>
 cudaError_t launch_nt(const DecodeParams& p, const Plan& P, cudaStream_t st) {
   if (P.mode == kOne) return launch_one<T, D, FMT, NT, kOne>(p, P, st);

@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kSlotThreads) k_kv_slots(SlotArgs a, bool clus
   int* s_ctx = s_first + a.B + 1;    // [B] cached tokens
   __shared__ uint32_t s_warp[32];
 
+  after_previous();
   const int P = a.page_size;
   const int room = a.max_pages * P;  // < 2^31 (checked by the caller)
   int used = *a.free_used;
@@ -173,24 +174,8 @@ cudaError_t launch_kv_slots(const SlotArgs& a, cudaStream_t st) {
   const bool in_place = a.seq_lens == a.ctx_lens || a.free_used_out == a.free_used;
   const int ctas = static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, (items + kSlotThreads - 1) / kSlotThreads),
                                                       in_place ? kSlotCluster : kSlotCtas));
-  const bool cluster = in_place && ctas > 1;
-  if (!cluster) {
-    k_kv_slots<<<ctas, kSlotThreads, smem, st>>>(a, false);
-    return cudaGetLastError();
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kSlotThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_kv_slots, a, true);
+  const int cluster = in_place ? ctas : 1;
+  return launch_after(k_kv_slots, dim3(ctas), kSlotThreads, smem, st, cluster, a, cluster > 1);
 }
 
 // ------------------------------------------------------------ k_kv_append
@@ -288,6 +273,7 @@ struct PageDiv {
 template <typename T, int D, int FMT, bool MEAN>
 __global__ void __launch_bounds__(kAppendThreads, 6) k_kv_append(const AppendArgs a, const PageDiv div) {
   constexpr int LANES = D / 16;                  // threads a row
+  after_previous();
   const int c = threadIdx.x % LANES;
   const int h = blockIdx.y;
   const int t = blockIdx.x * (kAppendThreads / LANES) + threadIdx.x / LANES;
@@ -393,9 +379,8 @@ cudaError_t append_fmt(const AppendArgs& a, cudaStream_t st) {
   PageDiv div;
   div.shift = 31 - __builtin_clz(a.c.page_size - 1);  // page_size >= 16
   div.mul = static_cast<uint32_t>(((uint64_t(1) << (32 + div.shift)) + a.c.page_size - 1) / a.c.page_size);
-  if (a.mean_k != nullptr) k_kv_append<T, D, FMT, true><<<grid, kAppendThreads, 0, st>>>(a, div);
-  else k_kv_append<T, D, FMT, false><<<grid, kAppendThreads, 0, st>>>(a, div);
-  return cudaGetLastError();
+  if (a.mean_k != nullptr) return launch_after(k_kv_append<T, D, FMT, true>, grid, kAppendThreads, 0, st, 1, a, div);
+  return launch_after(k_kv_append<T, D, FMT, false>, grid, kAppendThreads, 0, st, 1, a, div);
 }
 
 template <typename T, int D>

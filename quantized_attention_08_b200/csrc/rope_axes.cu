@@ -69,6 +69,7 @@ __device__ __forceinline__ uint4 rope_ld(const void* p) {
 
 template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) k_rope_axes(RopeArgs a, int heads_per_cta) {
+  after_previous();
   const int units = a.d / 16;  // threads a token
   const int64_t item = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / units) + threadIdx.x / units;
   const int u = threadIdx.x % units;
@@ -153,14 +154,9 @@ cudaError_t launch_rope_axes(const RopeArgs& a, cudaStream_t st) {
   const int want = static_cast<int>(std::min<int64_t>((4 * 148 + gx - 1) / gx, (heads + kRopeUnroll - 1) / kRopeUnroll));
   const int hpc = ((heads + want - 1) / want + kRopeUnroll - 1) / kRopeUnroll * kRopeUnroll;
   const dim3 grid(static_cast<unsigned>(gx), (heads + hpc - 1) / hpc);
-  if (a.bf16) {
-    if (a.interleaved) k_rope_axes<__nv_bfloat16, true><<<grid, kRopeThreads, 0, st>>>(a, hpc);
-    else k_rope_axes<__nv_bfloat16, false><<<grid, kRopeThreads, 0, st>>>(a, hpc);
-  } else {
-    if (a.interleaved) k_rope_axes<__half, true><<<grid, kRopeThreads, 0, st>>>(a, hpc);
-    else k_rope_axes<__half, false><<<grid, kRopeThreads, 0, st>>>(a, hpc);
-  }
-  return cudaGetLastError();
+  auto* f = a.bf16 ? (a.interleaved ? k_rope_axes<__nv_bfloat16, true> : k_rope_axes<__nv_bfloat16, false>)
+                   : (a.interleaved ? k_rope_axes<__half, true> : k_rope_axes<__half, false>);
+  return launch_after(f, grid, kRopeThreads, 0, st, 1, a, hpc);
 }
 
 }  // namespace sage

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <utility>
 
 #include "sage.h"
 
@@ -29,6 +30,36 @@ class OncePerDevice {
  private:
   std::atomic<bool> done_[64] = {};
 };
+
+#if defined(__CUDACC__)
+// A launch that may be placed while the kernel before it in the stream ends: the
+// kernel begins with after_previous(), which waits for that one's end and for
+// its writes.  Every block passes it, so that a kernel's end implies the end of
+// all before it.  (A step is a chain of kernels of a few microseconds: their
+// launches hide about a microsecond each in the ends of the ones before.)
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// cluster: CTAs of a thread-block cluster, 1 for none.
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster,
+                         Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+#endif
 
 struct SlotArgs {
   const int32_t* ctx_lens;

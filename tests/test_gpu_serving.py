@@ -675,3 +675,69 @@ def test_prefill_then_decode_steps(sage, fmt):
     # the decode kernel's row for the prompts' last tokens agrees with the prefill's
     last = torch.stack([o0[:, prompt[0] - 1], o0[:, T0 - 1]])
     assert bool(torch.isfinite(last).all())
+
+
+@pytest.mark.parametrize("fmt,B,n0", [("8+8", 2, 40), ("16", 70, 30), ("8+8", 70, 120)])
+def test_captured_step_equals_eager_steps(sage, fmt, B, n0):
+    """A decode step -- slots in place, rope, append, attention, each on what the
+    one before it wrote -- captured once and replayed, against the same steps
+    issued one by one: the same tokens, cache and outputs, bit for bit.  The
+    steps run back to back, so that their kernels' launches overlap."""
+    d, H, Hk, P, steps, dtype = 128, 8, 2, 16, 25, torch.bfloat16
+    g = gen(n0 + B)
+    sections = [16, 24, 24]
+    inv = torch.cat([10000.0 ** (-torch.arange(n, device="cuda") / n) for n in sections]).float()
+    width, pages = 16, 16 * B
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    toks = [(rand(B, H, 1, d), rand(B, Hk, 1, d), rand(Hk, B, d)) for _ in range(steps)]
+    first = (rand(Hk, B * n0, d), rand(Hk, B * n0, d))
+    free = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    mean = torch.randn(B, Hk, d, generator=g, device="cuda")
+
+    def start():
+        c = sage.SageKVCache.allocate(pages, Hk, P, d, fmt, dtype)
+        s = dict(c=c, lens=ints([0] * B), used=ints([0]), table=torch.full((B, width), -1, dtype=torch.int32, device="cuda"),
+                 one=ints([1] * B), cu=ints([0] * (B + 1)), slots=ints([0] * B), pos=ints([0] * B), ids=ints([0] * B),
+                 q=toks[0][0].clone(), k=toks[0][1].clone(), v=toks[0][2].clone())
+        lens, _, slots, _, ids, used = sage.sage_kv_slots(s["lens"], ints([n0] * B), free, s["used"], s["table"],
+                                                          page_size=P, T=B * n0)
+        s["lens"].copy_(lens)
+        s["used"].copy_(used)
+        sage.sage_kv_append(*first, slots, c, mean_k=mean, seq_ids=ids)
+        return s
+
+    def step(s):
+        sage.sage_kv_slots(s["lens"], s["one"], free, s["used"], s["table"], page_size=P, T=B,
+                           out=(s["lens"], s["cu"], s["slots"], s["pos"], s["ids"], s["used"]))
+        pos = torch.stack([s["pos"]] * 3)[:, :, None]
+        q, k = sage.sage_rope_axes(s["q"], s["k"], pos, inv, sections)
+        sage.sage_kv_append(k[:, :, 0].transpose(0, 1), s["v"], s["slots"], s["c"], mean_k=mean, seq_ids=s["ids"])
+        return sage.sage_attn_decode_paged(q, s["c"], s["table"], s["lens"], width * P)
+
+    eager, want = start(), []
+    for q, k, v in toks:
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            eager[name].copy_(t)
+        want.append(step(eager))
+        torch.cuda.synchronize()  # one by one
+    warm = start()
+    step(warm)
+    replayed = start()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(replayed)
+    got = []
+    for q, k, v in toks:
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            replayed[name].copy_(t)
+        graph.replay()
+        got.append(out.clone())
+    torch.cuda.synchronize()
+    assert replayed["lens"].tolist() == [n0 + steps] * B
+    for name in ("lens", "used", "table", "slots"):
+        assert torch.equal(eager[name], replayed[name]), name
+    for a, b in zip(want, got):
+        assert same_bits(a, b) and bool(torch.isfinite(a).all())
+    for a, b in ((eager["c"].k, replayed["c"].k), (eager["c"].v, replayed["c"].v)):
+        assert same_bits(a, b)
