@@ -22,22 +22,21 @@
 // with bulk copies of whole rows (a step of a page is one run of memory for
 // each of K, V and the scales), counted by an mbarrier a stage.  cp.async by the
 // lanes that later read the bytes, in fragment order, reached 4.9 TB/s where
-// rows in order reach 6.5 (eight lanes then touch two to four lines at once);
-// copies issued by the consuming warps themselves cost those a third of their
-// instructions.  A stage is released once K is multiplied and V is in registers.
+// rows in order reach 6.5 (eight lanes then touch two to four lines at once).
+// A stage is released once K is multiplied and V is in registers.
 //
 // Products.  mma.sync m16n8k16, transposed: S^T = K q^T and O^T = V^T P^T,
 // with tokens (channels) on the 16 side and query rows on the 8 side, since
 // one token's group has 1 to 8 rows; 16 rows a tile would compute twice as
-// much for nothing.  The tcgen05 form has 128 rows at least; at one to eight
-// rows the tensor work here is a few percent of what HBM leaves time for.
+// much for nothing.  The tcgen05 forms have 64 rows at least; at one to sixteen
+// the tensor pipe is 10 to 18 percent busy.
 // The order of k inside the products is free, so a lane's 16-byte pieces of
 // K's rows serve as fragments as they are; pairs of V's rows are interleaved
 // with prmt.  int8 and E4M3 codes become fp16 numbers exactly; delta_K multiplies
 // the fp32 scores, delta_V, in units of the largest one so far, the
-// probabilities.  S, m, l, O are fp32;
-// P is rounded to 16 bits for its product (2^-12 or 2^-9 relative, as every
-// 16-bit attention does), l sums the unrounded values.
+// probabilities.  S, m, l, O are fp32; P is rounded to 16 bits for its product
+// (half a step, 2^-11 or 2^-8 relative, as every 16-bit attention does), l sums
+// the unrounded values.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -232,8 +231,8 @@ struct Step {
 inline __host__ __device__ int steps_of(int len, int tok) { return (len + tok - 1) / tok; }
 // places of a segment in the line
 inline __host__ __device__ int places_of(int len, int tok) { return len > 0 ? steps_of(len, tok) + kSegmentCost : 0; }
-// places of a worker
-// (at least total / workers; fp32 rounded up, since a 64-bit division is slow)
+// places of a worker: at least total / workers (fp32 rounded up, since a 64-bit
+// division is slow), the same number wherever it is asked for
 __device__ __forceinline__ int64_t per_worker(int64_t total, int workers) {
   const int64_t per = static_cast<int64_t>(ceilf(__fdiv_ru(__ll2float_ru(total), static_cast<float>(workers))));
   return per > kMinSteps ? per : kMinSteps;
@@ -296,16 +295,12 @@ __device__ __forceinline__ Stretch stretch_of(const DecodeParams& p, const Reque
     }
     const int places = q.places[lo + 1] - q.places[lo];
     int64_t in = at - static_cast<int64_t>(q.places[lo]) * HZ;
-    int z = static_cast<int>(__ll2float_rn(in) / static_cast<float>(places));  // off by one at most
-    z = min(z, HZ - 1);
+    // in / places by fp32 (a 64-bit division is slow), then put right: it is off by
+    // one at most for any head count below 2^22
+    int z = min(static_cast<int>(__ll2float_rn(in) / static_cast<float>(places)), HZ - 1);
     in -= static_cast<int64_t>(z) * places;
-    if (in < 0) {
-      --z;
-      in += places;
-    } else if (in >= places) {
-      ++z;
-      in -= places;
-    }
+    for (; in < 0; in += places) --z;
+    for (; in >= places; in -= places) ++z;
     const int place = static_cast<int>(in);
     w.cur.b = lo;
     w.cur.z = z;
@@ -348,9 +343,9 @@ __device__ __forceinline__ void next_segment(const DecodeParams& p, const Reques
   c.len = (c.steps - 1) * S::TOK + 1 + q.last[c.b];
 }
 
-// The loading warp: lane w feeds the ring of warp w, so that one instruction
-// stream serves all of them.  The page numbers of a lane's next step are read
-// while the current one is copied.
+// A loading warp: each of its lanes feeds the ring of one consuming warp, so that
+// one instruction stream serves several.  The page numbers of a lane's next step
+// are read while the current one is copied.
 template <typename S, Mode MODE>
 __device__ __forceinline__ void feed(const DecodeParams& p, const Requests& q, uint8_t* smem, uint64_t* full,
                                      uint64_t* empty, uint32_t* absent, volatile int* abort_flag, int feeder,
@@ -607,7 +602,10 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
   }
   if (threadIdx.x == 0) s_abort = 0;
   after_previous();  // and before the join may be placed: it reads the lengths while this grid runs
-  if (MODE == kCluster) cluster_arrive();  // before the first remote store, all CTAs have started
+  if (MODE == kCluster) {  // before the first remote store, all CTAs have started
+    __syncwarp();
+    cluster_arrive();
+  }
   if (MODE == kLine) {
     // the join's CTAs may be placed now; they wait for this grid's end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -34,8 +34,8 @@ class OncePerDevice {
 #if defined(__CUDACC__)
 // A launch that may be placed while the kernel before it in the stream ends: the
 // kernel begins with after_previous(), which waits for that one's end and for
-// its writes.  Every block passes it, so that a kernel's end implies the end of
-// all before it.  (A step is a chain of kernels of a few microseconds: their
+// its writes.  Every block with work passes it, so that a kernel's end implies
+// the end of all before it.  (A step is a chain of kernels of a few microseconds: their
 // launches hide about a microsecond each in the ends of the ones before.)
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
