@@ -76,7 +76,8 @@ constexpr int kMaxCluster = 8;      // portable
 constexpr int kClusterSteps = 4, kClusterStepsFew = 2, kClusterFew = 32;
 constexpr int kClusterCtas = 128, kCluster8Ctas = 64;
 // What beginning a segment costs, in steps: the line counts each segment as that
-// much longer, so that a warp with many short ones gets fewer steps.
+// much longer, so that a warp with many short ones gets fewer steps (64 ragged
+// requests 8+8: 102 us with 1, 97 with 2, 97 with 3).
 constexpr int kSegmentCost = 2;
 
 struct DecodeParams {
@@ -1059,8 +1060,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
 // a row by itself; with more (or one row a CTA, where rows are few) the warps
 // share each row's pieces and are added in order.  Either way the order of the
 // sum depends on the sizes alone.  Rows of requests without tokens are zeros.
-constexpr int kJoinWarps = 8;
-constexpr int kJoinLoads = 8;
+constexpr int kJoinLoads = 12;
 constexpr int kMaxPieces = kSms * kWarps;  // a segment has at most one of each worker
 
 // kJoinLoads pieces of a row (a lane's D / 32 channels of each): i0, i0 + stride, ...
@@ -1090,13 +1090,13 @@ __device__ __forceinline__ void load_pieces(float (*x)[D / 32], const float* po,
   }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const DecodeParams p, int rows_per_group, int per_cta,
+template <typename T, int D, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) k_attn_join(const DecodeParams p, int rows_per_group, int per_cta,
                                                                 int parts) {
   constexpr int PER = D / 32;
   __shared__ float s_w[kMaxPieces];
-  __shared__ float s_o[kJoinWarps][D];
-  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+  __shared__ float s_o[WARPS][D];
+  __shared__ float s_m[WARPS], s_l[WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int HZ = p.Hk * p.groups;
   // grid: x = segment of the request and part of its rows, y = request
@@ -1113,7 +1113,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const DecodeParam
   // The lengths are inputs: the steps before this request and in all are
   // counted while the pieces are still being computed.
   int before = 0, all = 0;
-  for (int i = threadIdx.x; i < p.B; i += kJoinWarps * 32) {
+  for (int i = threadIdx.x; i < p.B; i += WARPS * 32) {
     const int v = places_of(clamp_len(p, p.lens[i]), p.step_tokens);
     all += v;
     if (i < b) before += v;
@@ -1123,19 +1123,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const DecodeParam
     all += __shfl_xor_sync(0xffffffffu, all, o);
     before += __shfl_xor_sync(0xffffffffu, before, o);
   }
-  __shared__ int2 s_steps[kJoinWarps];
+  __shared__ int2 s_steps[WARPS];
   if (lane == 0) s_steps[warp] = make_int2(before, all);
   __syncthreads();
   before = all = 0;
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     before += s_steps[w].x;
     all += s_steps[w].y;
   }
   const int places = places_of(clamp_len(p, p.lens[b]), p.step_tokens);
   after_previous();
   if (places == 0) {
-    for (int rg = first + warp; rg < last; rg += kJoinWarps) {
+    for (int rg = first + warp; rg < last; rg += WARPS) {
       const int64_t out = out_of(rg);
       uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(p.o) + out * D);
       for (int i = lane; i < D / 2; i += 32) dst[i] = 0;
@@ -1155,7 +1155,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const DecodeParam
   const int64_t piece = static_cast<int64_t>(rows_per_group) * D;
 
   if (n <= (per_cta > 1 ? 32 : kJoinLoads)) {
-    for (int rg = first + warp; rg < last; rg += kJoinWarps) {
+    for (int rg = first + warp; rg < last; rg += WARPS) {
       const float2 own = lane < n ? ml[(2 * lane + (lane == 0 ? late : 0)) * rows_per_group + rg]
                                   : make_float2(-INFINITY, 0.f);
       const float* row = po + static_cast<int64_t>(rg) * D;
@@ -1189,26 +1189,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const DecodeParam
   }
 
   for (int rg = first; rg < last; ++rg) {
-    constexpr int kOwn = (kMaxPieces + kJoinWarps * 32 - 1) / (kJoinWarps * 32);
+    constexpr int kOwn = (kMaxPieces + WARPS * 32 - 1) / (WARPS * 32);
     float2 own[kOwn];
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kOwn; ++j) {
-      const int i = threadIdx.x + j * kJoinWarps * 32;
+      const int i = threadIdx.x + j * WARPS * 32;
       own[j] = i < n ? ml[(2 * i + (i == 0 ? late : 0)) * rows_per_group + rg] : make_float2(-INFINITY, 0.f);
       m = fmaxf(m, own[j].x);
     }
     const float* row = po + static_cast<int64_t>(rg) * D;
     float x[kJoinLoads][PER];
-    load_pieces<D>(x, row, piece, late, warp, kJoinWarps, n);
+    load_pieces<D>(x, row, piece, late, warp, WARPS, n);
     m = warp_max(m);
     if (lane == 0) s_m[warp] = m;
     __syncthreads();
-    m = warp_max(s_m[lane % kJoinWarps]);
+    m = warp_max(s_m[lane % WARPS]);
     float l = 0.f;
 #pragma unroll
     for (int j = 0; j < kOwn; ++j) {
-      const int i = threadIdx.x + j * kJoinWarps * 32;
+      const int i = threadIdx.x + j * WARPS * 32;
       if (i < n) {
         const float w = own[j].x == -INFINITY ? 0.f : exp2_fast(own[j].x - m);
         l += own[j].y * w;
@@ -1224,14 +1224,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const DecodeParam
     for (int i0 = warp;;) {
 #pragma unroll
       for (int j = 0; j < kJoinLoads; ++j) {
-        const int i = i0 + j * kJoinWarps;
+        const int i = i0 + j * WARPS;
         const float f = i < n ? s_w[i] : 0.f;
 #pragma unroll
         for (int e = 0; e < PER; ++e) o[e] += f * x[j][e];
       }
-      i0 += kJoinWarps * kJoinLoads;
+      i0 += WARPS * kJoinLoads;
       if (i0 >= n) break;
-      load_pieces<D>(x, row, piece, late, i0, kJoinWarps, n);
+      load_pieces<D>(x, row, piece, late, i0, WARPS, n);
     }
 #pragma unroll
     for (int e = 0; e < PER; ++e) s_o[warp][lane * PER + e] = o[e];
@@ -1239,7 +1239,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_attn_join(const DecodeParam
     if (threadIdx.x < D / 2) {
       float ll = 0.f, a0 = 0.f, a1 = 0.f;
 #pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) {
+      for (int w = 0; w < WARPS; ++w) {
         ll += s_l[w];
         a0 += s_o[w][2 * threadIdx.x];
         a1 += s_o[w][2 * threadIdx.x + 1];
@@ -1327,8 +1327,11 @@ cudaError_t launch_one(const DecodeParams& p, const Plan& P, cudaStream_t st) {
   int per_cta = in_group;
   while (per_cta > 1 && segments * ((in_group + per_cta - 1) / per_cta) < 2 * kSms) per_cta = (per_cta + 1) / 2;
   const int parts = (in_group + per_cta - 1) / per_cta;
-  return launch_after(k_attn_join<T, D>, dim3(parts * p.groups * p.Hk, p.B), kJoinWarps * 32, 0, st, 1, p, 8 * NT,
-                      per_cta, parts);
+  const dim3 join_grid(parts * p.groups * p.Hk, p.B);
+  // a warp a row, or eight on one row
+  if (per_cta > 1 && per_cta <= 4)
+    return launch_after(k_attn_join<T, D, 4>, join_grid, 4 * 32, 0, st, 1, p, 8 * NT, per_cta, parts);
+  return launch_after(k_attn_join<T, D, 8>, join_grid, 8 * 32, 0, st, 1, p, 8 * NT, per_cta, parts);
 }
 template <typename T, int D, int FMT, int NT>
 cudaError_t launch_nt(const DecodeParams& p, const Plan& P, cudaStream_t st) {
