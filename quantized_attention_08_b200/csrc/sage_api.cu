@@ -51,6 +51,11 @@ sage_status_t from_cuda(cudaError_t e) {
   return SAGE_ERR_CUDA;
 }
 
+sage_status_t launched(const char* step, cudaError_t e) {
+  if (e != cudaSuccess) sage::set_error_detail(step, e);
+  return from_cuda(e);
+}
+
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // Layout of the intermediates inside one workspace.
@@ -830,7 +835,7 @@ sage_status_t sage_kv_slots(const int32_t* ctx_lens, const int32_t* new_lens, in
   a.max_pages = max_pages;
   a.page_size = page_size;
   a.T = T;
-  return from_cuda(sage::launch_kv_slots(a, static_cast<cudaStream_t>(stream)));
+  return launched("launch of sage_kv_slots", sage::launch_kv_slots(a, static_cast<cudaStream_t>(stream)));
 }
 
 sage_status_t sage_rope_axes(const void* q, const int64_t* q_strides, void* q_out,
@@ -887,7 +892,7 @@ sage_status_t sage_rope_axes(const void* q, const int64_t* q_strides, void* q_ou
   a.bf16 = dtype == SAGE_BF16;
   sage_status_t s = check_device();
   if (s != SAGE_OK) return s;
-  return from_cuda(sage::launch_rope_axes(a, static_cast<cudaStream_t>(stream)));
+  return launched("launch of sage_rope_axes", sage::launch_rope_axes(a, static_cast<cudaStream_t>(stream)));
 }
 
 sage_status_t sage_kv_append(const void* k, const int64_t* k_strides, const void* v,
@@ -918,7 +923,7 @@ sage_status_t sage_kv_append(const void* k, const int64_t* k_strides, const void
   a.B = B;
   a.c = *cache;
   if ((s = check_device()) != SAGE_OK) return s;
-  return from_cuda(sage::launch_kv_append(a, static_cast<cudaStream_t>(stream)));
+  return launched("launch of sage_kv_append", sage::launch_kv_append(a, static_cast<cudaStream_t>(stream)));
 }
 
 size_t sage_attn_decode_workspace_bytes(int B, int H, int H_kv, int n_q, int d, int max_len,
@@ -949,7 +954,11 @@ sage_status_t sage_attn_decode_paged(const void* q, const int64_t* q_strides,
   }
   const size_t need = sage::decode_workspace_bytes(B, H, cache->H_kv, n_q, cache->d, max_len, cache->format);
   if (need > 0) {
-    if (ws_bytes < need) return SAGE_ERR_NO_MEMORY;
+    if (ws_bytes < need) {
+      sage::set_error_detail("sage_attn_decode_paged: workspace smaller than sage_attn_decode_workspace_bytes()",
+                             cudaErrorInvalidValue, static_cast<int>(need > 0x7FFFFFFF ? 0x7FFFFFFF : need));
+      return SAGE_ERR_NO_MEMORY;
+    }
     if (!workspace) return SAGE_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return SAGE_ERR_MISALIGNED;
   }
@@ -969,7 +978,8 @@ sage_status_t sage_attn_decode_paged(const void* q, const int64_t* q_strides,
   a.sm_scale = sm_scale;
   a.timeout_ns = g_timeout_ns.load();
   if ((s = check_device()) != SAGE_OK) return s;
-  return from_cuda(sage::launch_attn_decode(a, static_cast<cudaStream_t>(stream)));
+  return launched("launch of sage_attn_decode_paged",
+                  sage::launch_attn_decode(a, static_cast<cudaStream_t>(stream)));
 }
 
 int sage_v_hat_layout(void) { return 0; }

@@ -81,6 +81,8 @@ def test_decode_refusals(lib):
     assert call(max_pages=1000, max_len=60000, ws=P(OK + 16)) == 3 and call(max_pages=1000, max_len=60000, ws=None) == 1
     need = lib.sage_attn_decode_workspace_bytes(3, 8, 2, 1, 128, 60000, 2)
     assert need > 0 and call(max_pages=1000, max_len=60000, bytes=need - 1) == 7
+    import quantized_attention_08_b200 as pkg
+    assert "workspace smaller" in pkg.sage_last_error_detail()
     assert call(B=0, q=None, lens=None, o=None) == 0 and call(nq=0, q=None, o=None) == 0
 
 
@@ -131,7 +133,7 @@ def test_rope_refusals(lib):
     assert call(B=0, q=None) == 0 and call(N=0, q=None) == 0
 
 
-def test_binding_refusals():
+def test_binding_refusals(lib):
     import quantized_attention_08_b200 as sage
     h = lambda *s: torch.zeros(*s, dtype=torch.float16)  # noqa: E731
     i = lambda *s: torch.zeros(*s, dtype=torch.int32)    # noqa: E731
