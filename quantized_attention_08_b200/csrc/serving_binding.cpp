@@ -58,7 +58,7 @@ void check_device(const at::Tensor& t, at::Device dev, const char* name) {
 void check_strided(const at::Tensor& t, at::ScalarType type, const char* name, at::Device dev) {
   check_type(t, type, name);
   check_device(t, dev, name);
-  if (t.dim() == 0 || t.stride(-1) != 1)
+  if (t.dim() == 0 || (t.stride(-1) != 1 && t.size(-1) > 1))
     TORCH_CHECK_VALUE(false, name, " must be dense along its last axis");
 }
 

@@ -677,6 +677,43 @@ def test_prefill_then_decode_steps(sage, fmt):
     assert bool(torch.isfinite(last).all())
 
 
+def test_given_outputs_and_refusals(sage):
+    """Outputs and workspaces that the caller brings, strides of one-entry axes,
+    and what the binding refuses on the device."""
+    c, table, K, V = filled_cache(sage, [40, 7], 2, 16, 64, "8+8", torch.bfloat16, seed=1)
+    lens = ints([40, 7])
+    q = torch.randn(2, 4, 64, generator=gen(2), device="cuda").bfloat16()
+    o = torch.full_like(q, 9.0)
+    got = sage.sage_attn_decode_paged(q, c, table, lens, 40, o=o)
+    assert got.data_ptr() == o.data_ptr() and same_bits(got, sage.sage_attn_decode_paged(q, c, table, lens, 40))
+    check_decode((got[:, :, None], plain_decode(q[:, :, None], K, V, [40, 7], True, 0.125)[1].float()),
+                 plain_decode(q[:, :, None], K, V, [40, 7], True, 0.125))
+    refused = [dict(q=q.half()), dict(q=q[..., :32]), dict(table=table[:1]), dict(lens=lens.long()), dict(lens=lens.cpu()),
+               dict(o=o[:1]), dict(o=o.transpose(0, 1).contiguous().transpose(0, 1)), dict(max_len=1 << 31)]
+    for kw in refused:
+        a = dict(q=q, table=table, lens=lens, max_len=40, o=None)
+        a.update(kw)
+        with pytest.raises((TypeError, ValueError)):
+            sage.sage_attn_decode_paged(a["q"], c, a["table"], a["lens"], a["max_len"], o=a["o"])
+    with pytest.raises(sage.SageError) as e:
+        sage.sage_attn_decode_paged(q, c, table, lens, table.shape[1] * 16 + 1)
+    assert e.value.status == 1
+    with pytest.raises(sage.SageError) as e:  # rows of q that are not 16-byte aligned
+        sage.sage_attn_decode_paged(torch.zeros(2, 4, 68, device="cuda").bfloat16()[..., :64], c, table, lens, 40)
+    assert e.value.status == 3
+    k = torch.zeros(2, 3, 64, device="cuda").bfloat16()
+    for kw in (dict(slots=ints([0, 1])), dict(v=k[:1]), dict(mean_k=torch.zeros(1, 2, 64, device="cuda"))):
+        with pytest.raises(ValueError):
+            sage.sage_kv_append(k, kw.pop("v", k), kw.pop("slots", ints([0, 1, 2])), c, **kw)
+    # one token a sequence: the strides of its axis are whatever they are
+    inv = torch.ones(32, device="cuda")
+    pos = ints([[3, 5], [7, 9]]).t()[None, :, :1]  # [1, 2, 1], last stride 2
+    x = torch.randn(2, 1, 4, 64, generator=gen(3), device="cuda").bfloat16().transpose(1, 2)
+    out, none = sage.sage_rope_axes(x, None, pos, inv, [32])
+    check_rope(out, x, pos, inv, [32], "half")
+    assert none is None
+
+
 @pytest.mark.parametrize("fmt,B,n0", [("8+8", 2, 40), ("16", 70, 30), ("8+8", 70, 120)])
 def test_captured_step_equals_eager_steps(sage, fmt, B, n0):
     """A decode step -- slots in place, rope, append, attention, each on what the
