@@ -34,9 +34,9 @@
 // K's rows serve as fragments as they are; pairs of V's rows are interleaved
 // with prmt.  int8 and E4M3 codes become fp16 numbers exactly; delta_K multiplies
 // the fp32 scores, delta_V, in units of the largest one so far, the
-// probabilities.  S, m, l, O are fp32; P is rounded to 16 bits for its product
-// (half a step, 2^-11 or 2^-8 relative, as every 16-bit attention does), l sums
-// the unrounded values.
+// probabilities.  S, m, l, O are fp32; P enters its product as two 16-bit numbers
+// whose sum is within 2^-16 (bf16) or 2^-22 of it, or as one fp16 number where the
+// output is bf16 and V E4M3.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -59,6 +59,10 @@ constexpr int kFeeders = 4;   // loading warps
 constexpr int kMaxBatch = 4096;   // prefix sums in shared memory
 constexpr int kSms = 148;
 constexpr int kMinSteps = 2;      // of one warp's stretch
+// How far scores may pass the running maximum before it follows (in log2).  With 0,
+// some row of 8 or 16 grows in most steps of a stretch (four drafted tokens: 44.0 us;
+// 39.3 with 4, 39.1 with 8).
+constexpr float kSlack = 8.f;
 // How the segments are spread over the warps.
 enum Mode {
   kOne,     // a warp a segment
@@ -584,6 +588,11 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
   // int8 K and E4M3 V become fp16 whatever the model's type is
   using TK = typename std::conditional<FMT == SAGE_KV_16, T, __half>::type;
   using TV = typename std::conditional<FMT == SAGE_KV_8P8, __half, T>::type;
+  // P as the sum of two numbers of its 16-bit type, its rounding and what that
+  // leaves (to 2^-16 of it for bf16, 2^-22 for fp16): with one, the output's error was up to 1.5 times
+  // that of its own rounding.  E4M3 V under a bf16 model needs one: P is fp16 there,
+  // eight times as fine as the output.
+  constexpr bool kTwoParts = std::is_same<T, TV>::value;
   constexpr int ROWS = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t s_full[kWarps * kStages], s_empty[kWarps * kStages];
@@ -753,9 +762,10 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
       }
     if (p.causal) vis_min = cur.len - p.n_q + 1;
 
-    // m: largest score; l: sum of 2^(s - m).  O is summed in units of `unit`, the
-    // largest delta_V so far: P delta_V / unit is at most 1, whatever V's range, and
-    // what it loses below fp16's normal numbers is 2^-25 of the largest row of V.
+    // m: largest score, or one less by kSlack at most; l: sum of 2^(s - m).  O is
+    // summed in units of `unit`, the largest delta_V so far up to a factor of 16, so
+    // that P delta_V / unit fits fp16 whatever V's range; what it loses below fp16's
+    // normal numbers is 2^-25 of the largest row of V.
     float acc[NT][D / 16][4];
     float m[NT][2], l[NT][2];
     float unit = S::VS ? kTinyScale : 1.f, per_unit = S::VS ? 1.f / kTinyScale : 1.f;
@@ -899,7 +909,9 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
               if (t >= vis[n][e & 1] || (gone >> u & 1)) s[n][u][e] = -INFINITY;
             }
       }
-      // ---- running maxima: reduced over the lanes only when one grew
+      // ---- running maxima: reduced over the lanes, and O rescaled, only where a
+      // score has outgrown m by kSlack (in log2) or a delta_V the unit sixteenfold:
+      // P stays below 2^kSlack * 16, which fp16 holds as exactly as P below 1
       bool grew = false;
       float top[NT][2], top_v = 0.f;
 #pragma unroll
@@ -910,12 +922,12 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
 #pragma unroll
           for (int u = 1; u < S::SUB; ++u) t = fmaxf(t, fmaxf(s[n][u][e], s[n][u][e + 2]));
           top[n][e] = t;
-          grew |= t > m[n][e];
+          grew |= t > m[n][e] + kSlack;
         }
       if (S::VS) {
 #pragma unroll
         for (int u = 0; u < S::SUB; ++u) top_v = fmaxf(top_v, fmaxf(vs[u][0], vs[u][1]));
-        grew |= top_v > unit;
+        grew |= top_v > 16.f * unit;
       }
       if (__any_sync(0xffffffffu, grew)) {
         float down = 1.f;
@@ -946,7 +958,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
         }
       }
       // ---- probabilities and O^T += V^T P^T
-      uint32_t pf[NT][S::SUB][2];
+      uint32_t pf[NT][S::SUB][2], pl[NT][S::SUB][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float m0[2] = {m[n][0] == -INFINITY ? 0.f : m[n][0], m[n][1] == -INFINITY ? 0.f : m[n][1]};
@@ -962,8 +974,15 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
 #pragma unroll
             for (int i = 0; i < 4; ++i) e[i] *= f[i >> 1];
           }
-          pf[n][u][0] = transpose8x8(pack16<TV>(e[0], e[1]));
-          pf[n][u][1] = transpose8x8(pack16<TV>(e[2], e[3]));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t hi = pack16<TV>(e[2 * i], e[2 * i + 1]);
+            pf[n][u][i] = transpose8x8(hi);
+            if (kTwoParts) {
+              const float2 f = unpack16<TV>(hi);
+              pl[n][u][i] = transpose8x8(pack16<TV>(e[2 * i] - f.x, e[2 * i + 1] - f.y));
+            }
+          }
         }
       }
 #pragma unroll
@@ -977,8 +996,10 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
               const uint32_t a[4] = {bytes(w0, w1, 0x5410), bytes(w0, w1, 0x7632), bytes(w2, w3, 0x5410),
                                      bytes(w2, w3, 0x7632)};
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
+              for (int n = 0; n < NT; ++n) {
                 mma16816<TV>(acc[n][(VWORDS * x + i) % (D / 16)], a, pf[n][u][0], pf[n][u][1]);
+                if (kTwoParts) mma16816<TV>(acc[n][(VWORDS * x + i) % (D / 16)], a, pl[n][u][0], pl[n][u][1]);
+              }
             } else {
               uint32_t x01[4], x23[4];
               e4m3_pairs(w0, w1, x01);
@@ -987,8 +1008,11 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
               for (int y = 0; y < 2; ++y) {
                 const uint32_t a[4] = {x01[2 * y], x01[2 * y + 1], x23[2 * y], x23[2 * y + 1]};
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) {
                   mma16816<TV>(acc[n][(2 * (VWORDS * x + i) + y) % (D / 16)], a, pf[n][u][0], pf[n][u][1]);
+                  if (kTwoParts)
+                    mma16816<TV>(acc[n][(2 * (VWORDS * x + i) + y) % (D / 16)], a, pl[n][u][0], pl[n][u][1]);
+                }
               }
             }
           }
