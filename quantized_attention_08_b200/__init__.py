@@ -503,25 +503,21 @@ class SageKVCache:
         self.v_scale = v_scale if self.format == "8+8" else None
         self.num_pages, self.H_kv, self.page_size, self.d = k.shape
         s = self._struct = _CacheStruct()
-        for name, t, inner in (("k", k, k.shape[1:]), ("v", v, k.shape[1:]),
-                               ("k_scale", self.k_scale, k.shape[1:3]),
-                               ("v_scale", self.v_scale, k.shape[1:3])):
+        rows = self.H_kv * self.page_size
+        for name, t, page in (("k", k, rows * self.d), ("v", v, rows * self.d), ("k_scale", self.k_scale, rows),
+                              ("v_scale", self.v_scale, rows)):
             if t is None:
                 if (name == "k_scale" and self.format != "16") or (name == "v_scale" and self.format == "8+8"):
                     raise ValueError(f"a cache of format {self.format} needs {name}")
                 continue
-            if name.endswith("scale"):
-                if t.dtype != torch.float32 or t.shape != k.shape[:3]:
-                    raise ValueError(f"{name} must be fp32 [num_pages, H_kv, page_size]")
-            if t.device != self.device:
+            if name.endswith("scale") and (t.dtype != torch.float32 or t.shape != k.shape[:3]):
+                raise ValueError(f"{name} must be fp32 [num_pages, H_kv, page_size]")
+            if t.get_device() != self._dev:
                 raise ValueError(f"{name} must be on {self.device}")
-            if self.num_pages and not t[0].is_contiguous():
+            if not t.is_contiguous() and self.num_pages and not t[0].is_contiguous():
                 raise ValueError(f"a page of {name} must be contiguous")
-            n = 1
-            for x in inner:
-                n *= x
             setattr(s, name, t.data_ptr())
-            setattr(s, name + "_page_stride", t.stride(0) if self.num_pages > 1 else n)
+            setattr(s, name + "_page_stride", t.stride(0) if self.num_pages > 1 else page)
         s.num_pages, s.H_kv, s.page_size, s.d = k.shape
         s.format, s.dtype = KV_FORMATS[self.format], _DTYPES[model]
         self._ref = _c.addressof(s)

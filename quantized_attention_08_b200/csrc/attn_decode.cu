@@ -6,9 +6,10 @@
 //
 // Bound by HBM: each visible key and value is read once and serves all G
 // query heads of its group (and all query tokens).  Measured on one B200,
-// device time with the join: 89.5 us for one request of 131072 tokens (H 32,
-// H_kv 8, d 128, bf16: 537 MB, 0.91 of the measured copy rate), 95.2 us for 64
-// requests of 1 to 8192 tokens in 8+8 (570 MB, 0.91).
+// device time with the join: 90.5 us for one request of 131072 tokens (H 32,
+// H_kv 8, d 128, bf16: 537 MB, 0.90 of the measured copy rate), 93.5 us for 64
+// requests of 1 to 8192 tokens in 8+8 (570 MB, 0.93; 107 us for seconds on end,
+// when the power cap lowers the clock).
 //
 // Work.  The cache of one (request, kv head, group of query rows) is a
 // segment of steps of S::TOK tokens.  All segments' steps stand in one line,
