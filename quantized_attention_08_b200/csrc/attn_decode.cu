@@ -35,9 +35,16 @@
 // K's rows serve as fragments as they are; pairs of V's rows are interleaved
 // with prmt.  int8 and E4M3 codes become fp16 numbers exactly; delta_K multiplies
 // the fp32 scores, delta_V, in units of the largest one so far, the
-// probabilities.  S, m, l, O are fp32; P enters its product as two 16-bit numbers
-// whose sum is within 2^-16 (bf16) or 2^-22 of it, or as one fp16 number where the
-// output is bf16 and V E4M3.
+// probabilities.  S, m, l, O are fp32.  P enters its product as two 16-bit numbers,
+// its rounding and what that leaves, which is within 2^-16 of it.  For bf16 that is
+// all; fp16 has few exponents, so P is taken in its upper range (2^10 or 2^11 is the
+// largest when m is new), and where a P is so small that its second number would
+// lose bits, a step's second numbers are taken 2^11 times as large and their sums
+// put right.  What is lost then is at most 2^-47 of the largest P (with delta_V
+// 2^-46 of the largest P times the largest delta_V).  One number instead of two
+// made the output's error up to 1.5 times that of its own rounding, and lost the keys 17
+// nats below the largest.  64 requests of 8+8: 97.5 us fp16, 103 bf16 (99 with one
+// number); four drafted tokens, bf16: 42.6 (39.3).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -62,8 +69,17 @@ constexpr int kSms = 148;
 constexpr int kMinSteps = 2;      // of one warp's stretch
 // How far scores may pass the running maximum before it follows (in log2).  With 0,
 // some row of 8 or 16 grows in most steps of a stretch (four drafted tokens: 44.0 us;
-// 39.3 with 4, 39.1 with 8).
-constexpr float kSlack = 8.f;
+// 39.3 with 4, 39.1 with 8, all with one number a P).  A larger one costs fp16 P its range.
+constexpr float kSlack = 4.f;
+// How many times the unit of O delta_V may be before it follows.
+constexpr float kUnitSlack = 2.f;
+// Where fp16 P stands: 2^15 is the largest it gets.
+constexpr float kLift = 15.f - kSlack, kLiftV = kLift - 1.f;
+// How much larger the second numbers of small P are, and which are small: a number
+// that is below fp16's normal ones is off by 2^-25, which is 2^-16 of 2^-9.  Below
+// 2^-37 nothing of a P is left either way.
+constexpr float kApart = 2048.f;
+constexpr uint32_t kSmall = (127 - 9) << 23, kNothing = (127 - 37) << 23;  // as the bits of a float
 // How the segments are spread over the warps.
 enum Mode {
   kOne,     // a warp a segment
@@ -173,6 +189,13 @@ __device__ __forceinline__ void e4m3_pairs(uint32_t a, uint32_t b, uint32_t* out
   asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;}"
       : "=r"(out[2]), "=r"(out[3])
       : "r"(y));
+}
+
+// two fp16 numbers / kApart
+__device__ __forceinline__ uint32_t over_apart(uint32_t a) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x10001000u));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -589,11 +612,8 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
   // int8 K and E4M3 V become fp16 whatever the model's type is
   using TK = typename std::conditional<FMT == SAGE_KV_16, T, __half>::type;
   using TV = typename std::conditional<FMT == SAGE_KV_8P8, __half, T>::type;
-  // P as the sum of two numbers of its 16-bit type, its rounding and what that
-  // leaves (to 2^-16 of it for bf16, 2^-22 for fp16): with one, the output's error was up to 1.5 times
-  // that of its own rounding.  E4M3 V under a bf16 model needs one: P is fp16 there,
-  // eight times as fine as the output.
-  constexpr bool kTwoParts = std::is_same<T, TV>::value;
+  constexpr bool kHalfP = std::is_same<TV, __half>::value;
+  constexpr float kUp = !kHalfP ? 0.f : FMT == SAGE_KV_8P8 ? kLiftV : kLift;
   constexpr int ROWS = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t s_full[kWarps * kStages], s_empty[kWarps * kStages];
@@ -647,15 +667,15 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
   }
   __syncthreads();
   // Two tiles of rows need more registers than 12 warps get at launch: the four
-  // loading warps give theirs up (72 + 2 * 216 = 3 * 168).
+  // loading warps give theirs up (56 + 2 * 224 = 3 * 168).
   constexpr bool kShift = NT > 1;
   if (warp >= kWarps) {
-    if (kShift) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (kShift) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     feed<S, MODE>(p, q, smem, s_full, s_empty, s_absent, &s_abort, warp - kWarps, lane);
     return;
   }
 
-  if (kShift) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+  if (kShift) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
   Stretch st = stretch_of<S, MODE>(p, q, warp);
   if (MODE == kLine ? st.left <= 0 : st.cur.b < 0) return;
   Cursor& cur = st.cur;
@@ -763,10 +783,9 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
       }
     if (p.causal) vis_min = cur.len - p.n_q + 1;
 
-    // m: largest score, or one less by kSlack at most; l: sum of 2^(s - m).  O is
-    // summed in units of `unit`, the largest delta_V so far up to a factor of 16, so
-    // that P delta_V / unit fits fp16 whatever V's range; what it loses below fp16's
-    // normal numbers is 2^-25 of the largest row of V.
+    // m: kUp below the largest score, or below one less by kSlack at most; l: sum of
+    // 2^(s - m).  O is summed in units of `unit`, the largest delta_V so far up to a
+    // factor of kUnitSlack, so that P delta_V / unit fits fp16 whatever V's range.
     float acc[NT][D / 16][4];
     float m[NT][2], l[NT][2];
     float unit = S::VS ? kTinyScale : 1.f, per_unit = S::VS ? 1.f / kTinyScale : 1.f;
@@ -911,8 +930,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
             }
       }
       // ---- running maxima: reduced over the lanes, and O rescaled, only where a
-      // score has outgrown m by kSlack (in log2) or a delta_V the unit sixteenfold:
-      // P stays below 2^kSlack * 16, which fp16 holds as exactly as P below 1
+      // score has outgrown m by kSlack (in log2) or a delta_V the unit
       bool grew = false;
       float top[NT][2], top_v = 0.f;
 #pragma unroll
@@ -923,12 +941,12 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
 #pragma unroll
           for (int u = 1; u < S::SUB; ++u) t = fmaxf(t, fmaxf(s[n][u][e], s[n][u][e + 2]));
           top[n][e] = t;
-          grew |= t > m[n][e] + kSlack;
+          grew |= t > m[n][e] + (kSlack + kUp);
         }
       if (S::VS) {
 #pragma unroll
         for (int u = 0; u < S::SUB; ++u) top_v = fmaxf(top_v, fmaxf(vs[u][0], vs[u][1]));
-        grew |= top_v > 16.f * unit;
+        grew |= top_v > kUnitSlack * unit;
       }
       if (__any_sync(0xffffffffu, grew)) {
         float down = 1.f;
@@ -943,7 +961,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
           float alpha[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float t = fmaxf(token_max(top[n][e]), m[n][e]);
+            const float t = fmaxf(token_max(top[n][e]) - kUp, m[n][e]);
             alpha[e] = t == m[n][e] ? 1.f : exp2_fast(m[n][e] - t);
             m[n][e] = t;
             l[n][e] *= alpha[e];
@@ -959,64 +977,91 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
         }
       }
       // ---- probabilities and O^T += V^T P^T
-      uint32_t pf[NT][S::SUB][2], pl[NT][S::SUB][2];
+      uint32_t least = 0xffffffffu;  // the bits of the smallest P that counts, less kNothing
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float m0[2] = {m[n][0] == -INFINITY ? 0.f : m[n][0], m[n][1] == -INFINITY ? 0.f : m[n][1]};
 #pragma unroll
         for (int u = 0; u < S::SUB; ++u) {
-          float e[4];
+          float* const e = s[n][u];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[i] = exp2_fast(s[n][u][i] - m0[i & 1]);
+          for (int i = 0; i < 4; ++i) e[i] = exp2_fast(e[i] - m0[i & 1]);
           l[n][0] += e[0] + e[2];
           l[n][1] += e[1] + e[3];
           if (S::VS) {
             const float f[2] = {vs[u][0] * per_unit, vs[u][1] * per_unit};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] *= f[i >> 1];
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t hi = pack16<TV>(e[2 * i], e[2 * i + 1]);
-            pf[n][u][i] = transpose8x8(hi);
-            if (kTwoParts) {
-              const float2 f = unpack16<TV>(hi);
-              pl[n][u][i] = transpose8x8(pack16<TV>(e[2 * i] - f.x, e[2 * i + 1] - f.y));
+            for (int i = 0; i < 4; ++i) {
+              e[i] *= f[i >> 1];
             }
+          }
+          if (kHalfP) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) least = min(least, __float_as_uint(e[i]) - kNothing);
           }
         }
       }
+      const bool small = kHalfP && __any_sync(0xffffffffu, least < kSmall - kNothing);
+      const float rest = small ? kApart : 1.f;
+      uint32_t pf[NT][S::SUB][2], pl[NT][S::SUB][2];
 #pragma unroll
-      for (int u = 0; u < S::SUB; ++u)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int x = 0; x < S::VC; ++x)
+        for (int u = 0; u < S::SUB; ++u)
 #pragma unroll
-          for (int i = 0; i < VWORDS; ++i) {
-            const uint32_t w0 = vr[u][0][x][i], w1 = vr[u][1][x][i], w2 = vr[u][2][x][i], w3 = vr[u][3][x][i];
-            if (S::VB == 2) {
-              const uint32_t a[4] = {bytes(w0, w1, 0x5410), bytes(w0, w1, 0x7632), bytes(w2, w3, 0x5410),
-                                     bytes(w2, w3, 0x7632)};
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t hi = pack16<TV>(s[n][u][2 * i], s[n][u][2 * i + 1]);
+            const float2 f = unpack16<TV>(hi);
+            pf[n][u][i] = transpose8x8(hi);
+            pl[n][u][i] = transpose8x8(pack16<TV>((s[n][u][2 * i] - f.x) * rest, (s[n][u][2 * i + 1] - f.y) * rest));
+          }
+      // `apart`: the second numbers are kApart times as large
+      auto add_v = [&](auto apart) {
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                mma16816<TV>(acc[n][(VWORDS * x + i) % (D / 16)], a, pf[n][u][0], pf[n][u][1]);
-                if (kTwoParts) mma16816<TV>(acc[n][(VWORDS * x + i) % (D / 16)], a, pl[n][u][0], pl[n][u][1]);
-              }
-            } else {
-              uint32_t x01[4], x23[4];
-              e4m3_pairs(w0, w1, x01);
-              e4m3_pairs(w2, w3, x23);
+        for (int u = 0; u < S::SUB; ++u)
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const uint32_t a[4] = {x01[2 * y], x01[2 * y + 1], x23[2 * y], x23[2 * y + 1]};
+          for (int x = 0; x < S::VC; ++x)
+#pragma unroll
+            for (int i = 0; i < VWORDS; ++i) {
+              const uint32_t w0 = vr[u][0][x][i], w1 = vr[u][1][x][i], w2 = vr[u][2][x][i], w3 = vr[u][3][x][i];
+              if (S::VB == 2) {
+                const int tile = (VWORDS * x + i) % (D / 16);
+                const uint32_t a[4] = {bytes(w0, w1, 0x5410), bytes(w0, w1, 0x7632), bytes(w2, w3, 0x5410),
+                                       bytes(w2, w3, 0x7632)};
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                  mma16816<TV>(acc[n][(2 * (VWORDS * x + i) + y) % (D / 16)], a, pf[n][u][0], pf[n][u][1]);
-                  if (kTwoParts)
-                    mma16816<TV>(acc[n][(2 * (VWORDS * x + i) + y) % (D / 16)], a, pl[n][u][0], pl[n][u][1]);
+                  mma16816<TV>(acc[n][tile], a, pf[n][u][0], pf[n][u][1]);
+                  if (decltype(apart)::value) {  // sums of their own
+                    float low[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma16816<TV>(low, a, pl[n][u][0], pl[n][u][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[n][tile][e] += low[e] * (1.f / kApart);
+                  } else {
+                    mma16816<TV>(acc[n][tile], a, pl[n][u][0], pl[n][u][1]);
+                  }
+                }
+              } else {
+                uint32_t x01[4], x23[4];
+                e4m3_pairs(w0, w1, x01);
+                e4m3_pairs(w2, w3, x23);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const int tile = (2 * (VWORDS * x + i) + y) % (D / 16);
+                  uint32_t a[4] = {x01[2 * y], x01[2 * y + 1], x23[2 * y], x23[2 * y + 1]};
+#pragma unroll
+                  for (int n = 0; n < NT; ++n) mma16816<TV>(acc[n][tile], a, pf[n][u][0], pf[n][u][1]);
+                  if (decltype(apart)::value) {  // V / kApart, exactly: E4M3's numbers are multiples of 2^-9
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a[e] = over_apart(a[e]);
+                  }
+#pragma unroll
+                  for (int n = 0; n < NT; ++n) mma16816<TV>(acc[n][tile], a, pl[n][u][0], pl[n][u][1]);
                 }
               }
             }
-          }
+      };
+      if (kHalfP && small) add_v(std::integral_constant<bool, kHalfP>());
+      else add_v(std::false_type());
     }
 
     // ---- end of the piece
