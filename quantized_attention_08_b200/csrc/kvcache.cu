@@ -111,9 +111,9 @@ __global__ void __launch_bounds__(kSlotThreads) k_kv_slots(SlotArgs a, bool clus
     run += total;
   }
   __syncthreads();
+  // in place: every CTA has read the old values
   if (cluster) cg::this_cluster().sync();
   const int rank = blockIdx.x, ctas = gridDim.x;
-  if (ctas > 1) cg::this_cluster().sync();
 
   const int have = a.num_free - used;  // pages left in the free list
   const int wanted = s_first[a.B];
