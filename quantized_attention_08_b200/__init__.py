@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 from typing import Optional
 
@@ -480,17 +481,23 @@ class SageKVCache:
     follows from the types: "16" (k and v fp16 or bf16), "B" (k int8 with
     k_scale, v 16-bit), "8+8" (k int8, v uint8 E4M3 codes, both scales; `dtype`
     is that of the model, fp16 unless given).  The tensors are the caller's
-    and are used in place."""
+    and are used in place, at the addresses that they have when the handle is
+    made: a cache of other tensors takes another handle."""
+
+    # read-only, since the calls go by the addresses and sizes in _struct
+    k, v, k_scale, v_scale, num_pages, page_size, H_kv, d, format, dtype, device = (
+        property(operator.attrgetter("_" + n)) for n in (
+            "k", "v", "k_scale", "v_scale", "num_pages", "page_size", "H_kv", "d", "format", "dtype", "device"))
 
     def __init__(self, k, v, k_scale=None, v_scale=None, dtype: Optional[torch.dtype] = None):
         if k.dim() != 4 or v.shape != k.shape:
             raise ValueError("k and v must both be [num_pages, H_kv, page_size, d]")
         if k.dtype in _DTYPES and v.dtype == k.dtype:
-            self.format, model = "16", k.dtype
+            fmt, model = "16", k.dtype
         elif k.dtype == torch.int8 and v.dtype in _DTYPES:
-            self.format, model = "B", v.dtype
+            fmt, model = "B", v.dtype
         elif k.dtype == torch.int8 and v.dtype == torch.uint8:
-            self.format, model = "8+8", dtype or torch.float16
+            fmt, model = "8+8", dtype or torch.float16
         else:
             raise TypeError(f"no cache format has k {k.dtype} and v {v.dtype}")
         if model not in _DTYPES or (dtype is not None and dtype != model):
@@ -498,29 +505,33 @@ class SageKVCache:
         if not k.is_cuda:
             raise TypeError("k must be a CUDA tensor")
         self._dev = k.get_device()
-        self.k, self.v, self.dtype, self.device = k, v, model, k.device
-        self.k_scale = k_scale if self.format != "16" else None
-        self.v_scale = v_scale if self.format == "8+8" else None
-        self.num_pages, self.H_kv, self.page_size, self.d = k.shape
+        k_scale = k_scale if fmt != "16" else None
+        v_scale = v_scale if fmt == "8+8" else None
+        self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
+        self._format, self._dtype, self._device = fmt, model, k.device
+        self._num_pages, self._H_kv, self._page_size, self._d = pages, heads, page_size, d = k.shape
         s = self._struct = _CacheStruct()
-        rows = self.H_kv * self.page_size
-        for name, t, page in (("k", k, rows * self.d), ("v", v, rows * self.d), ("k_scale", self.k_scale, rows),
-                              ("v_scale", self.v_scale, rows)):
+        rows = heads * page_size
+        for name, t, page in (("k", k, rows * d), ("v", v, rows * d), ("k_scale", k_scale, rows),
+                              ("v_scale", v_scale, rows)):
             if t is None:
-                if (name == "k_scale" and self.format != "16") or (name == "v_scale" and self.format == "8+8"):
-                    raise ValueError(f"a cache of format {self.format} needs {name}")
+                if (name == "k_scale" and fmt != "16") or (name == "v_scale" and fmt == "8+8"):
+                    raise ValueError(f"a cache of format {fmt} needs {name}")
                 continue
             if name.endswith("scale") and (t.dtype != torch.float32 or t.shape != k.shape[:3]):
                 raise ValueError(f"{name} must be fp32 [num_pages, H_kv, page_size]")
             if t.get_device() != self._dev:
-                raise ValueError(f"{name} must be on {self.device}")
-            if not t.is_contiguous() and self.num_pages and not t[0].is_contiguous():
+                raise ValueError(f"{name} must be on {k.device}")
+            if not t.is_contiguous() and pages and not t[0].is_contiguous():
                 raise ValueError(f"a page of {name} must be contiguous")
             setattr(s, name, t.data_ptr())
-            setattr(s, name + "_page_stride", t.stride(0) if self.num_pages > 1 else page)
+            setattr(s, name + "_page_stride", t.stride(0) if pages > 1 else page)
         s.num_pages, s.H_kv, s.page_size, s.d = k.shape
-        s.format, s.dtype = KV_FORMATS[self.format], _DTYPES[model]
+        s.format, s.dtype = KV_FORMATS[fmt], _DTYPES[model]
         self._ref = _c.addressof(s)
+
+    def __reduce__(self):  # copies are made of the tensors, not of the addresses
+        return SageKVCache, (self._k, self._v, self._k_scale, self._v_scale, self._dtype)
 
     @classmethod
     def allocate(cls, num_pages: int, H_kv: int, page_size: int, d: int, format: str = "8+8",
