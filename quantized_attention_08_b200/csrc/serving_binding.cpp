@@ -87,6 +87,12 @@ int c_int(int64_t v, const char* name) {
   return static_cast<int>(v);
 }
 
+bool truth(PyObject* o) {
+  const int t = PyObject_IsTrue(o);
+  if (t < 0) throw python_error();
+  return t != 0;
+}
+
 sage_dtype_t model_type(at::ScalarType t, const char* name) {
   if (t == at::kHalf) return SAGE_F16;
   if (t == at::kBFloat16) return SAGE_BF16;
@@ -214,7 +220,7 @@ PyObject* rope_axes(PyObject*, PyObject* const* a, Py_ssize_t) {
     TORCH_CHECK_VALUE(false, "positions must be [", A, ", ", N, "] or [", A, ", ", B, ", ", N, "], got ",
                       show(pos.sizes()));
   const void* inv = dense(a[3], at::kFloat, "inv_freq", dev, {R});
-  const int interleaved = PyObject_IsTrue(a[5]);
+  const int interleaved = truth(a[5]);
   const Launch launch(dev);
   const int s = f_rope(p[0], strides[0], p[1], strides[1], p[2], strides[2], p[3], strides[3],
                        static_cast<const int32_t*>(pos.data_ptr()), pos_strides, static_cast<const float*>(inv),
@@ -289,7 +295,7 @@ PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t) {
   const void* table_p = dense(table, at::kInt, "block_table", dev, {B, table.size(1)});
   const void* lens = dense(a[4], at::kInt, "seq_lens", dev, {B});
   const int max_len = c_int(a[5], "max_len");
-  const int causal = PyObject_IsTrue(a[6]);
+  const int causal = truth(a[6]);
   double scale = 1.0 / std::sqrt(static_cast<double>(c->d));
   if (a[7] != Py_None) {
     scale = PyFloat_AsDouble(a[7]);
@@ -303,7 +309,7 @@ PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t) {
     o = tensor(a[8], "o");
     dense(o, q.scalar_type(), "o", dev, q.sizes());
   }
-  const bool want_lse = PyObject_IsTrue(a[9]) == 1;
+  const bool want_lse = truth(a[9]);
   if (want_lse) lse = at::empty(q.sizes().slice(0, nd - 1), q.options().dtype(at::kFloat));
   void* ws_p = nullptr;
   size_t ws_bytes = 0;
