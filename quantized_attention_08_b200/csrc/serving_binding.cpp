@@ -272,6 +272,9 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t) {
   const int64_t ks[2] = {k.stride(0), k.stride(1)}, vs[2] = {v.stride(0), v.stride(1)};
   const void* slots = dense(a[2], at::kInt, "slot_map", dev, {T});
   const Launch launch(dev);
+  // no request has a mean: no token has one (an empty tensor's address is null,
+  // which the library takes for keys that are not smoothed)
+  if (a[5] != Py_None && B == 0) return status(SAGE_OK);
   return status(f_append(k.data_ptr(), ks, v.data_ptr(), vs, c_int(T, "T"), static_cast<const int32_t*>(slots),
                          static_cast<const float*>(mean), static_cast<const int32_t*>(ids), c_int(B, "B"), c,
                          launch.stream));

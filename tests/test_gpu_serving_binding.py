@@ -31,3 +31,14 @@ def test_flags_without_a_truth_value(sage):
     # two-element tensors have no truth value either
     with pytest.raises(RuntimeError, match="more than one value"):
         sage.sage_attn_decode_paged(q, c, ints([[0, 1]]), ints([20]), 32, causal=ints([0, 1]))
+
+
+@pytest.mark.parametrize("fmt", ["16", "8+8"])
+def test_means_of_no_request(sage, fmt):
+    """Tokens whose request has no mean are skipped, also where no request has one."""
+    c = sage.SageKVCache.allocate(2, 2, 16, 64, fmt)
+    x = torch.ones(2, 3, 64, dtype=torch.float16, device="cuda")
+    for B in (0, 1):
+        mean = torch.ones(B, 2, 64, device="cuda")
+        sage.sage_kv_append(x, x, ints([0, 5, 9]), c, mean_k=mean, seq_ids=ints([B, -1, B + 7]))
+        assert not any(bool(t.any()) for t in (c.k, c.v, c.k_scale, c.v_scale) if t is not None), B
