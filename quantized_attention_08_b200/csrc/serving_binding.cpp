@@ -110,6 +110,16 @@ struct Launch {
   void* stream;
 };
 
+// The library's call with the interpreter free for other threads: a launch waits
+// where the stream's queue is full.
+template <typename F>
+int free_call(F f) {
+  PyThreadState* const state = PyEval_SaveThread();
+  const int s = f();  // C functions: nothing is thrown
+  PyEval_RestoreThread(state);
+  return s;
+}
+
 PyObject* status(int s) { return PyLong_FromLong(s); }
 
 // -------------------------------------------------------------------- calls
@@ -162,8 +172,11 @@ PyObject* kv_slots(PyObject*, PyObject* const* a, Py_ssize_t) {
     out = a[7];
   }
   THPObjectPtr held(out);
-  const int s = f_slots(ctx_p, new_p, c_int(B, "B"), free_p, c_int(F, "the number of free pages"), used_p, table_p,
-                        c_int(width, "max_pages"), page_size, p[0], p[1], p[2], p[3], p[4], T, p[5], launch.stream);
+  const int b = c_int(B, "B"), pages = c_int(F, "the number of free pages"), w = c_int(width, "max_pages");
+  const int s = free_call([&] {
+    return f_slots(ctx_p, new_p, b, free_p, pages, used_p, table_p, w, page_size, p[0], p[1], p[2], p[3], p[4], T, p[5],
+                   launch.stream);
+  });
   return s != SAGE_OK ? status(s) : held.release();
   END_HANDLE_TH_ERRORS
 }
@@ -222,11 +235,14 @@ PyObject* rope_axes(PyObject*, PyObject* const* a, Py_ssize_t) {
   const void* inv = dense(a[3], at::kFloat, "inv_freq", dev, {R});
   const int interleaved = truth(a[5]);
   const Launch launch(dev);
-  const int s = f_rope(p[0], strides[0], p[1], strides[1], p[2], strides[2], p[3], strides[3],
-                       static_cast<const int32_t*>(pos.data_ptr()), pos_strides, static_cast<const float*>(inv),
-                       sections, static_cast<int>(A), c_int(B, "B"), c_int(H, "H"),
-                       has_k ? c_int(t[2].size(-3), "H_kv") : 0, c_int(N, "N"), c_int(d, "d"), interleaved, code,
-                       launch.stream);
+  const int b = c_int(B, "B"), h = c_int(H, "H"), hk = has_k ? c_int(t[2].size(-3), "H_kv") : 0, n = c_int(N, "N"),
+            ch = c_int(d, "d");
+  const int32_t* const pos_p = static_cast<const int32_t*>(pos.data_ptr());
+  const int s = free_call([&] {
+    return f_rope(p[0], strides[0], p[1], strides[1], p[2], strides[2], p[3], strides[3], pos_p, pos_strides,
+                  static_cast<const float*>(inv), sections, static_cast<int>(A), b, h, hk, n, ch, interleaved, code,
+                  launch.stream);
+  });
   if (s != SAGE_OK) return status(s);
   THPObjectPtr out(PyTuple_New(2));
   if (!out) throw python_error();
@@ -275,9 +291,12 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t) {
   // no request has a mean: no token has one (an empty tensor's address is null,
   // which the library takes for keys that are not smoothed)
   if (a[5] != Py_None && B == 0) return status(SAGE_OK);
-  return status(f_append(k.data_ptr(), ks, v.data_ptr(), vs, c_int(T, "T"), static_cast<const int32_t*>(slots),
-                         static_cast<const float*>(mean), static_cast<const int32_t*>(ids), c_int(B, "B"), c,
-                         launch.stream));
+  const void *k_p = k.data_ptr(), *v_p = v.data_ptr();
+  const int n = c_int(T, "T"), b = c_int(B, "B");
+  return status(free_call([&] {
+    return f_append(k_p, ks, v_p, vs, n, static_cast<const int32_t*>(slots), static_cast<const float*>(mean),
+                    static_cast<const int32_t*>(ids), b, c, launch.stream);
+  }));
   END_HANDLE_TH_ERRORS
 }
 
@@ -329,10 +348,14 @@ PyObject* attn_decode(PyObject*, PyObject* const* a, Py_ssize_t) {
     ws_p = ws.data_ptr();
     ws_bytes = ws.nbytes();
   }
-  const int s = f_decode(q.data_ptr(), qs, c, static_cast<const int32_t*>(table_p),
-                         c_int(table.size(1), "max_pages"), static_cast<const int32_t*>(lens), B, H, n_q, max_len,
-                         causal, static_cast<float>(scale), o.data_ptr(),
-                         want_lse ? lse.data_ptr<float>() : nullptr, ws_p, ws_bytes, launch.stream);
+  const int width = c_int(table.size(1), "max_pages");
+  const void* const q_p = q.data_ptr();
+  void* const o_p = o.data_ptr();
+  float* const lse_p = want_lse ? lse.data_ptr<float>() : nullptr;
+  const int s = free_call([&] {
+    return f_decode(q_p, qs, c, static_cast<const int32_t*>(table_p), width, static_cast<const int32_t*>(lens), B, H,
+                    n_q, max_len, causal, static_cast<float>(scale), o_p, lse_p, ws_p, ws_bytes, launch.stream);
+  });
   if (s != SAGE_OK) return status(s);
   THPObjectPtr out(THPVariable_Wrap(o));
   if (!out || !want_lse) return out.release();

@@ -1,4 +1,7 @@
 """GPU tests of what the serving calls' Python side does around the library."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -42,3 +45,43 @@ def test_means_of_no_request(sage, fmt):
         mean = torch.ones(B, 2, 64, device="cuda")
         sage.sage_kv_append(x, x, ints([0, 5, 9]), c, mean_k=mean, seq_ids=ints([B, -1, B + 7]))
         assert not any(bool(t.any()) for t in (c.k, c.v, c.k_scale, c.v_scale) if t is not None), B
+
+
+def test_other_threads_run_while_the_queue_is_full(sage):
+    """A call whose launch waits for room in the stream's queue does not hold the
+    interpreter: behind a kernel of half a second or more, thousands of calls
+    block, and this thread goes on meanwhile."""
+    c = sage.SageKVCache.allocate(2, 1, 16, 64, "16")
+    x, slot = torch.ones(1, 1, 64, dtype=torch.float16, device="cuda"), ints([3])
+    q, pos, inv = x[None], ints([[1]]), torch.ones(32, device="cuda")
+    lens, table, ws = ints([4]), ints([[0]]), torch.empty(256, dtype=torch.uint8, device="cuda")
+    out = tuple(ints([0] * n) for n in (1, 2, 1, 1, 1, 1))
+    o = torch.empty_like(q)
+    calls = [lambda: sage.sage_kv_append(x, x, slot, c),
+             lambda: sage.sage_rope_axes(q, None, pos, inv, [32], q_out=o),
+             lambda: sage.sage_kv_slots(ints_lens, one, free, used, table, page_size=16, T=1, out=out),
+             lambda: sage.sage_attn_decode_paged(q, c, table, lens, 4, o=o, workspace=ws)]
+    ints_lens, one, free, used = ints([0]), ints([1]), ints([0, 1]), ints([0])
+    for call in calls:
+        call()
+        torch.cuda.synchronize()
+        done = []
+
+        def work():
+            torch.cuda._sleep(1_000_000_000)  # clock cycles: half a second at 1965 MHz
+            at = time.perf_counter()
+            for _ in range(3000):
+                call()
+            done.append(time.perf_counter() - at)
+
+        t = threading.Thread(target=work)
+        t.start()
+        longest, last = 0.0, time.perf_counter()
+        while not done:
+            time.sleep(0.001)
+            now = time.perf_counter()
+            longest, last = max(longest, now - last), now
+        t.join()
+        torch.cuda.synchronize()
+        assert done[0] > 0.3, "the queue did not fill"
+        assert longest < 0.15, (longest, done)
