@@ -125,6 +125,16 @@ PyObject* status(int s) { return PyLong_FromLong(s); }
 // -------------------------------------------------------------------- calls
 // Each returns the status of the C call as an int if it is not SAGE_OK.
 
+// Entries [first, first + n) of a dense tensor without a gradient.  (Six dispatched
+// as_strided calls took 1.6 us where this takes next to nothing: the call 7.8 us, 6.1.)
+at::Tensor part(const at::Tensor& whole, int64_t first, int64_t n) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(whole.storage()),
+                                                          whole.key_set(), whole.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(first);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return t;
+}
+
 // (ctx_lens, new_lens, free_pages, free_used, block_table, page_size, T, out)
 PyObject* kv_slots(PyObject*, PyObject* const* a, Py_ssize_t) {
   HANDLE_TH_ERRORS
@@ -148,17 +158,17 @@ PyObject* kv_slots(PyObject*, PyObject* const* a, Py_ssize_t) {
   const Launch launch(dev);
   PyObject* out;
   if (a[7] == Py_None) {
-    // one allocation, six parts of it
-    int64_t all = 0;
-    for (int64_t n : sizes) all += n;
-    const at::Tensor whole = at::empty({all}, ctx.options());
+    // two allocations: what a request keeps from step to step, and the step's tokens
+    const at::Tensor whole[2] = {at::empty({2 * B + 2}, ctx.options()),
+                                 at::empty({3 * static_cast<int64_t>(T)}, ctx.options())};
     THPObjectPtr tuple(PyTuple_New(6));
     if (!tuple) throw python_error();
-    int64_t at_ = 0;
+    int64_t used[2] = {0, 0};
     for (int i = 0; i < 6; ++i) {
-      p[i] = whole.data_ptr<int32_t>() + at_;
-      PyTuple_SET_ITEM(tuple.get(), i, THPVariable_Wrap(whole.as_strided({sizes[i]}, {1}, at_)));
-      at_ += sizes[i];
+      const int w = i >= 2 && i < 5;
+      p[i] = whole[w].data_ptr<int32_t>() + used[w];
+      PyTuple_SET_ITEM(tuple.get(), i, THPVariable_Wrap(part(whole[w], used[w], sizes[i])));
+      used[w] += sizes[i];
     }
     out = tuple.release();
   } else {

@@ -85,3 +85,19 @@ def test_other_threads_run_while_the_queue_is_full(sage):
         torch.cuda.synchronize()
         assert done[0] > 0.3, "the queue did not fill"
         assert longest < 0.15, (longest, done)
+
+
+def test_kept_lengths_keep_no_tokens(sage):
+    """The results that go on to the next step hold no memory of the step's tokens."""
+    T = 20000
+    got = sage.sage_kv_slots(ints([3, 9]), ints([7, 2]), ints([4, 5, 6]), ints([0]), ints([[0, -1], [1, -1]]),
+                             page_size=16, T=T)
+    assert [len(t) for t in got] == [2, 3, T, T, T, 1]
+    lens, cu, slots, pos, ids, used = got
+    assert max(t.untyped_storage().nbytes() for t in (lens, cu, used)) <= 64
+    assert lens.tolist() == [10, 11] and cu.tolist() == [0, 7, 9] and used.tolist() == [0]
+    assert slots[:9].tolist() == list(range(3, 10)) + [25, 26] and slots[9:].unique().tolist() == [-1]
+    assert pos[:9].tolist() == list(range(3, 10)) + [9, 10] and ids[:9].tolist() == [0] * 7 + [1] * 2
+    for a in (lens, slots, used):  # parts of one allocation stay apart
+        a.fill_(77)
+    assert cu.tolist() == [0, 7, 9] and pos[:2].tolist() == [3, 4] and ids[-1].item() == -1
