@@ -289,13 +289,17 @@ sage_status_t sage_attn_fwd_varlen(const void* q, const void* k, const void* v, 
  *   sage_rope_axes  rotary positions of the step's Q and K
  *   sage_kv_append  the step's K and V, smoothed and quantized, into the cache
  *   sage_attn_decode_paged  attention of the new tokens over the cache
- * (prompts attend through sage_attn_fwd_varlen, whose pre-pass also gives the
- * mean_k that the cache's K is smoothed by).  These entry points take fp16 and
- * bf16.  Lengths, tables, slots and positions are read on the device, so that
+ * (fp16 prompts attend through sage_attn_fwd_varlen, whose pre-pass also gives
+ * the mean_k that the cache's K is smoothed by; neither takes bf16).  These entry
+ * points take fp16 and bf16.  Lengths, tables, slots and positions are read on the device, so that
  * a step can be captured in a CUDA graph and replayed as the requests grow.
  * None of them allocates device memory or keeps state.  Stride arrays are in
  * host memory and read before the call returns; the stride of an axis of one
- * entry is ignored.
+ * entry is ignored.  Values that are not finite are outside the contract here too:
+ * 8-bit codes do not keep them, and a V that is not finite may reach every query row
+ * of its request, rows that do not see its token among them.  What stands in slots
+ * behind a request's last token, or in pages that no request holds, is no input and
+ * may be anything.
  */
 typedef enum { SAGE_F16 = 0, SAGE_BF16 = 1 } sage_dtype_t;
 
@@ -421,9 +425,13 @@ sage_status_t sage_kv_append(const void* k, const int64_t* k_strides, const void
  *              (NULL if that is 0); holds no state between calls, but calls that may
  *              overlap need one each
  * Tokens on a page outside the cache count as absent.  Entries of block_table
- * behind a request's last page are not read, nor are slots behind its last
- * token.  Results do not depend on what else runs, and two calls on the same
- * inputs agree bit for bit.  B <= 4096, n_q * H / H_kv <= 1024.
+ * behind a request's last page are not read.  Slots behind its last token, on the
+ * same page, may be read and change nothing; so another stream may write them
+ * meanwhile.  Scores, sums and the softmax are fp32; a probability enters its product
+ * with V to within 2^-16 of itself and, for fp16 and for "8+8", to 2^-46 of the largest one
+ * (in "8+8" of the largest one times the largest v_scale) where that is more.
+ * Results do not depend on what else runs, and two calls on the same inputs agree
+ * bit for bit.  B <= 4096, n_q * H / H_kv <= 1024.
  */
 sage_status_t sage_attn_decode_paged(const void* q, const int64_t* q_strides,
                                      const sage_kv_cache_t* cache, const int32_t* block_table,
