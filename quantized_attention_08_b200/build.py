@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libsage.so")
 SERVING = os.path.join(PKG, "_serving.so")
 SERVING_SOURCE = os.path.join(CSRC, "serving_binding.cpp")
 SOURCES = ["prepass.cu", "attn_sm100.cu", "kvcache.cu", "rope_axes.cu", "attn_decode.cu", "sage_api.cu"]
-HEADERS = ["sage_ptx.cuh", "sage_internal.h", "serve_internal.h", "quant_div.h", "quant_pair.cuh"]
+HEADERS = ["sage_ptx.cuh", "sage_internal.h", "serve_internal.h", "serve_math.cuh", "quant_div.h", "quant_pair.cuh"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",

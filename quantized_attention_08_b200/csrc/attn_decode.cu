@@ -54,18 +54,16 @@
 
 #include "sage_ptx.cuh"
 #include "serve_internal.h"
+#include "serve_math.cuh"
 
 namespace sage {
 
 namespace {
 
-// the smallest scale a cache holds beside 0 (2^-100)
-constexpr float kTinyScale = 7.88860905e-31f;
 constexpr int kWarps = 8;
 constexpr int kStages = 3;
 constexpr int kFeeders = 4;   // loading warps
 constexpr int kMaxBatch = 4096;   // prefix sums in shared memory
-constexpr int kSms = 148;
 constexpr int kMinSteps = 2;      // of one warp's stretch
 // How far scores may pass the running maximum before it follows (in log2).  With 0,
 // some row of 8 or 16 grows in most steps of a stretch (four drafted tokens: 44.0 us;
@@ -141,32 +139,8 @@ __device__ __forceinline__ void mma16816<__nv_bfloat16>(float* c, const uint32_t
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <typename T>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t pack16<__half>(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <>
-__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 __device__ __forceinline__ uint32_t bytes(uint32_t a, uint32_t b, uint32_t sel) {
   return __byte_perm(a, b, sel);
-}
-
-template <typename T>
-__device__ __forceinline__ float2 unpack16(uint32_t w);
-template <>
-__device__ __forceinline__ float2 unpack16<__half>(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-template <>
-__device__ __forceinline__ float2 unpack16<__nv_bfloat16>(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 // Four int8 codes as four fp16 numbers: code + 128 (0 .. 255) taken as fp16 bits
@@ -235,6 +209,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // -------------------------------------------------------- shapes of a step
+// Tokens of a step, about 8 KB of K and V.
+constexpr int step_tokens(int d, int format) {
+  return d == 128 ? (format == SAGE_KV_8P8 ? 32 : 16) : (format == SAGE_KV_8P8 ? 64 : 32);
+}
+
 template <int D, int FMT>
 struct Step {
   static constexpr int KB = FMT == SAGE_KV_16 ? 2 : 1;   // bytes of a K element
@@ -246,9 +225,8 @@ struct Step {
   static constexpr int VE = VW / VB;                     // channels of a piece
   static constexpr bool KS = FMT != SAGE_KV_16;
   static constexpr bool VS = FMT == SAGE_KV_8P8;
-  // 16-token tiles of a step: about 8 KB a step
-  static constexpr int SUB = D == 128 ? (FMT == SAGE_KV_8P8 ? 2 : 1) : (FMT == SAGE_KV_8P8 ? 4 : 2);
-  static constexpr int TOK = 16 * SUB;
+  static constexpr int TOK = step_tokens(D, FMT);
+  static constexpr int SUB = TOK / 16;                   // 16-token tiles of a step
   // a stage of the ring: K rows, V rows, K scales, V scales
   static constexpr int V_AT = TOK * KROW;
   static constexpr int KS_AT = V_AT + TOK * VROW;
@@ -1335,11 +1313,6 @@ struct Plan {
   Mode mode;
   size_t off_ml, bytes;
 };
-
-int step_tokens(int d, int format) {
-  const int sub = d == 128 ? (format == SAGE_KV_8P8 ? 2 : 1) : (format == SAGE_KV_8P8 ? 4 : 2);
-  return 16 * sub;
-}
 
 Plan plan_of(int B, int H, int H_kv, int n_q, int d, int max_len, int format) {
   Plan P = {};

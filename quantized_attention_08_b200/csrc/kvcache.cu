@@ -9,6 +9,7 @@
 
 #include "quant_pair.cuh"
 #include "serve_internal.h"
+#include "serve_math.cuh"
 
 namespace sage {
 
@@ -25,7 +26,6 @@ namespace cg = cooperative_groups;
 // last read of the old values from the first write of the new ones.
 constexpr int kSlotThreads = 512;
 constexpr int kSlotCluster = 8;  // portable
-constexpr int kSlotCtas = 148;
 constexpr int kSlotMaxBatch = 8192;
 constexpr uint32_t kSlotCap = 1u << 30;  // of a sum of tokens: T is at most this
 
@@ -173,7 +173,7 @@ cudaError_t launch_kv_slots(const SlotArgs& a, cudaStream_t st) {
   const int64_t items = std::max<int64_t>(a.T, a.B);  // there are at most as many new pages
   const bool in_place = a.seq_lens == a.ctx_lens || a.free_used_out == a.free_used;
   const int ctas = static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, (items + kSlotThreads - 1) / kSlotThreads),
-                                                      in_place ? kSlotCluster : kSlotCtas));
+                                                      in_place ? kSlotCluster : kSms));
   const int cluster = in_place ? ctas : 1;
   return launch_after(k_kv_slots, dim3(ctas), kSlotThreads, smem, st, cluster, a, cluster > 1);
 }
@@ -194,7 +194,6 @@ cudaError_t launch_kv_slots(const SlotArgs& a, cudaStream_t st) {
 // 0.96 of the measured copy rate; two or four rows a thread with the next one's
 // loads in flight took 70.6 and 82.5 (more registers, fewer warps).
 constexpr int kAppendThreads = 256;
-constexpr float kTinyScale = 7.88860905e-31f;  // 2^-100
 
 template <typename T>
 __device__ __forceinline__ uint64_t to_f2(uint32_t w);  // the two values of w as fp32 (exact)
@@ -207,16 +206,9 @@ __device__ __forceinline__ uint64_t to_f2<__nv_bfloat16>(uint32_t w) {
   return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 template <typename T>
-__device__ __forceinline__ uint32_t from_f2(uint64_t f);
-template <>
-__device__ __forceinline__ uint32_t from_f2<__half>(uint64_t f) {
-  const __half2 h = __float22half2_rn(f2_unpack(f));
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <>
-__device__ __forceinline__ uint32_t from_f2<__nv_bfloat16>(uint64_t f) {
-  const __nv_bfloat162 h = __float22bfloat162_rn(f2_unpack(f));
-  return *reinterpret_cast<const uint32_t*>(&h);
+__device__ __forceinline__ uint32_t from_f2(uint64_t f) {
+  const float2 x = f2_unpack(f);
+  return pack16<T>(x.x, x.y);
 }
 
 __device__ __forceinline__ uint4 ld_once(const void* p) {

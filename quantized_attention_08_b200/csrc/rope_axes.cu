@@ -12,13 +12,12 @@
 // eight pairs (16 channels) of one token, keeps their cosines and sines in
 // registers and walks over the heads, so that the angles cost nothing beside
 // the traffic and no table exists.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include <algorithm>
 
 #include "serve_internal.h"
+#include "serve_math.cuh"
 
 namespace sage {
 
@@ -26,29 +25,6 @@ constexpr int kRopeThreads = 256;
 // Heads loaded before the first is rotated: 2 heads take 88 us on H 16 + 16, N
 // 32768, d 128, fp16 (537 MB: 0.93 of the measured copy rate), 1 97, 4 93.
 constexpr int kRopeUnroll = 2;
-
-template <typename T>
-__device__ __forceinline__ float2 rope_unpack(uint32_t w);
-template <>
-__device__ __forceinline__ float2 rope_unpack<__half>(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-template <>
-__device__ __forceinline__ float2 rope_unpack<__nv_bfloat16>(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-template <typename T>
-__device__ __forceinline__ uint32_t rope_pack(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t rope_pack<__half>(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <>
-__device__ __forceinline__ uint32_t rope_pack<__nv_bfloat16>(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // x cos - y sin and y cos + x sin, each product and each sum rounded once
 __device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
@@ -125,7 +101,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_axes(RopeArgs a, int head
       if (turns) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float2 p = rope_unpack<T>(x[e]), q = rope_unpack<T>(y[e]);
+          float2 p = unpack16<T>(x[e]), q = unpack16<T>(y[e]);
           if (INTERLEAVED) {  // pairs are neighbours: e and 4 + e
             turn(p.x, p.y, cs[e], sn[e]);
             turn(q.x, q.y, cs[4 + e], sn[4 + e]);
@@ -133,8 +109,8 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_axes(RopeArgs a, int head
             turn(p.x, q.x, cs[2 * e], sn[2 * e]);
             turn(p.y, q.y, cs[2 * e + 1], sn[2 * e + 1]);
           }
-          x[e] = rope_pack<T>(p.x, p.y);
-          y[e] = rope_pack<T>(q.x, q.y);
+          x[e] = pack16<T>(p.x, p.y);
+          y[e] = pack16<T>(q.x, q.y);
         }
       }
       T* dst = static_cast<T*>(a.out[w]) + b * a.out_s[w][0] + h * a.out_s[w][1] + n * a.out_s[w][2];
@@ -151,7 +127,7 @@ cudaError_t launch_rope_axes(const RopeArgs& a, cudaStream_t st) {
   const int heads = a.heads[0] + a.heads[1];
   // All heads in one CTA when the tokens alone fill the GPU a few times over;
   // fewer heads a CTA otherwise, down to one unrolled group.
-  const int want = static_cast<int>(std::min<int64_t>((4 * 148 + gx - 1) / gx, (heads + kRopeUnroll - 1) / kRopeUnroll));
+  const int want = static_cast<int>(std::min<int64_t>((4 * kSms + gx - 1) / gx, (heads + kRopeUnroll - 1) / kRopeUnroll));
   const int hpc = ((heads + want - 1) / want + kRopeUnroll - 1) / kRopeUnroll * kRopeUnroll;
   const dim3 grid(static_cast<unsigned>(gx), (heads + hpc - 1) / hpc);
   auto* f = a.bf16 ? (a.interleaved ? k_rope_axes<__nv_bfloat16, true> : k_rope_axes<__nv_bfloat16, false>)

@@ -31,6 +31,10 @@ class OncePerDevice {
   std::atomic<bool> done_[64] = {};
 };
 
+constexpr int kSms = 148;
+// the smallest scale that a cache holds beside 0 (2^-100)
+constexpr float kTinyScale = 7.88860905e-31f;
+
 #if defined(__CUDACC__)
 // A launch that may be placed while the kernel before it in the stream ends: the
 // kernel begins with after_previous(), which waits for that one's end and for
