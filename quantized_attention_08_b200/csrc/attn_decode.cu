@@ -908,7 +908,9 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
             }
       }
       // ---- running maxima: reduced over the lanes, and O rescaled, only where a
-      // score has outgrown m by kSlack (in log2) or a delta_V the unit
+      // score has outgrown m by kSlack (in log2) or a delta_V the unit.  Directed
+      // roundings keep P within fp16 where scores are so large that their steps are not
+      // small beside kUp.
       bool grew = false;
       float top[NT][2], top_v = 0.f;
 #pragma unroll
@@ -919,7 +921,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
 #pragma unroll
           for (int u = 1; u < S::SUB; ++u) t = fmaxf(t, fmaxf(s[n][u][e], s[n][u][e + 2]));
           top[n][e] = t;
-          grew |= t > m[n][e] + (kSlack + kUp);
+          grew |= t > __fadd_rd(m[n][e], kSlack + kUp);
         }
       if (S::VS) {
 #pragma unroll
@@ -939,7 +941,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
           float alpha[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float t = fmaxf(token_max(top[n][e]) - kUp, m[n][e]);
+            const float t = fmaxf(__fadd_ru(token_max(top[n][e]), -kUp), m[n][e]);
             alpha[e] = t == m[n][e] ? 1.f : exp2_fast(m[n][e] - t);
             m[n][e] = t;
             l[n][e] *= alpha[e];
