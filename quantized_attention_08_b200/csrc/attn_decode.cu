@@ -590,6 +590,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
   // int8 K and E4M3 V become fp16 whatever the model's type is
   using TK = typename std::conditional<FMT == SAGE_KV_16, T, __half>::type;
   using TV = typename std::conditional<FMT == SAGE_KV_8P8, __half, T>::type;
+  constexpr bool kScaledQ = !std::is_same<T, TK>::value;
   constexpr bool kHalfP = std::is_same<TV, __half>::value;
   constexpr float kUp = !kHalfP ? 0.f : FMT == SAGE_KV_8P8 ? kLiftV : kLift;
   constexpr int ROWS = 8 * NT;
@@ -694,16 +695,17 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
     }
     float to_log2 = p.scale_log2;
     float base_s[NT][2];  // where a score's sum starts
+    float back[NT][2];    // of bf16 q that became fp16: each row's power of two
 #pragma unroll
     for (int n = 0; n < NT; ++n) base_s[n][0] = base_s[n][1] = 0.f;
     if (S::KB == 1) {
-      if (!std::is_same<T, TK>::value) {
-        // bf16 q to fp16, times the power of two that brings the largest of
-        // these rows to [2^13, 2^14): exact down to 2^-28 of it, and what is lost
-        // below is less than fp32 loses in the sum
-        float top = 0.f;
+      if (kScaledQ) {
+        // bf16 q to fp16, each row times the power of two that brings its largest to
+        // [2^13, 2^14): exact down to 2^-28 of it, and what is lost below is less than
+        // fp32 loses in the sum
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+          float top = 0.f;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -711,15 +713,14 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
               const float2 f = unpack16<T>(qf[n][i][e]);
               top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
             }
-        top = warp_max(top);
-        const int ex = static_cast<int>(__float_as_uint(top) >> 23 & 255);
-        const int k = top > 0.f ? min(127, 13 - (ex - 127)) : 0;  // >= -114
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-        // 2^-k, in two factors: k = 127 has no normal reciprocal
-        to_log2 *= __uint_as_float(static_cast<uint32_t>(127 - k / 2) << 23);
-        to_log2 *= __uint_as_float(static_cast<uint32_t>(127 - (k - k / 2)) << 23);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));  // of row g
+          const int ex = static_cast<int>(__float_as_uint(top) >> 23 & 255);
+          const int k = top > 0.f ? min(127, 13 - (ex - 127)) : 0;  // >= -115
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+          const float down = __uint_as_float(static_cast<uint32_t>(127 + 12 - k) << 23);  // 2^(12 - k)
+          back[n][0] = __shfl_sync(0xffffffffu, down, 8 * c);
+          back[n][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
 #pragma unroll
           for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -727,6 +728,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
               const float2 f = unpack16<T>(qf[n][i][e]);
               qf[n][i][e] = pack16<__half>(f.x * up, f.y * up);
             }
+        }
       }
       // code + 128, as the bits of an fp16 number, is (code + 128) 2^-24: the sums
       // start at -128 2^-24 sum q, and end 2^24 times too small
@@ -746,7 +748,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
         base_s[n][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
         base_s[n][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
       }
-      to_log2 *= 16777216.f;
+      to_log2 *= kScaledQ ? 4096.f : 16777216.f;  // half of the 2^24 is in `back`: neither leaves fp32
     }
     // keys visible to this lane's two rows of each tile
     int vis[NT][2];
@@ -891,8 +893,8 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
           const float f = S::KS ? to_log2 * ks[u][e] : to_log2;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            s[n][u][2 * e] *= f;
-            s[n][u][2 * e + 1] *= f;
+            s[n][u][2 * e] *= kScaledQ ? f * back[n][0] : f;
+            s[n][u][2 * e + 1] *= kScaledQ ? f * back[n][1] : f;
           }
         }
       // ---- masks: the end of the cache, later query tokens' keys, no page
