@@ -23,7 +23,9 @@ namespace cg = cooperative_groups;
 // block scans, one dependent read (an old table entry or a free page), the
 // stores.  Where seq_lens is ctx_lens or free_used_out is free_used (a captured
 // step that is replayed), the CTAs are one cluster, whose barrier separates the
-// last read of the old values from the first write of the new ones.
+// last read of the old values from the first write of the new ones; eight CTAs at
+// most then, which many places show: 256 places 3.5 us, in place 3.6; 4096 3.4 and
+// 4.2; 65536 3.9 and 15.0.
 constexpr int kSlotThreads = 512;
 constexpr int kSlotCluster = 8;  // portable
 constexpr int kSlotMaxBatch = 8192;
@@ -190,9 +192,10 @@ cudaError_t launch_kv_slots(const SlotArgs& a, cudaStream_t st) {
 // holds channels 8c .. and d/2 + 8c .. of a row, so that a row takes d / 16
 // lanes and its maximum log2(d / 16) shuffles; its loads do not wait for its
 // slot (a skipped token is read for nothing).  One row a thread and six CTAs an
-// SM: 65536 tokens of 8 heads, d 128, fp16 with means, 8+8 (407 MB) take 64.7 us,
-// 0.96 of the measured copy rate; two or four rows a thread with the next one's
-// loads in flight took 70.6 and 82.5 (more registers, fewer warps).
+// SM: 65536 tokens of 8 heads, d 128, fp16 with means, 8+8 (407 MB) take 67 us on the
+// device, 0.93 of the measured copy rate (69 to 72 in sequence, where the power cap
+// lowers the clock); two or four rows a thread with the next one's loads in flight
+// took 9 and 27% longer (more registers, fewer warps).
 constexpr int kAppendThreads = 256;
 
 template <typename T>
@@ -283,7 +286,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6) k_kv_append(const AppendArg
   const uint32_t vw[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
   const bool known = !MEAN || (seq >= 0 && seq < a.B);
   const bool live = slot >= 0 && slot < slots && known;
-  // read here, while K and V are on their way (78 us in place of 64.7 otherwise)
+  // read here, while K and V are on their way (a fifth longer otherwise)
   uint64_t mean[8];
   if (MEAN && known) {
     const float* m = a.mean_k + (static_cast<size_t>(seq) * a.c.H_kv + h) * D + 8 * c;

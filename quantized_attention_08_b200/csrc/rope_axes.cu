@@ -10,8 +10,10 @@
 //
 // Bound by HBM: every element is read once and written once.  A thread owns
 // eight pairs (16 channels) of one token, keeps their cosines and sines in
-// registers and walks over the heads, so that the angles cost nothing beside
-// the traffic and no table exists.
+// registers and walks over the heads, so that the angles cost little beside
+// the traffic and no table exists.  Few heads share them less: of the measured copy
+// rate 16 + 16 heads reach 0.92 (d 128, 400 to 540 MB each), 8 + 8 0.90, 4 + 1 0.84,
+// 1 + 1 0.61.
 #include <stdint.h>
 
 #include <algorithm>

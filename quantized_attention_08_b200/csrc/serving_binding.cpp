@@ -4,7 +4,7 @@
 // A decode step's kernels take two to ten microseconds; checking and passing
 // seventeen arguments through ctypes takes as long again as all of them, so these
 // four calls unpack torch's tensors here (host time a call: slot maps 14.7 us
-// through ctypes, 7.8 here; rope 15.9, 5.9; append 10.3, 4.6; decode 16.0, 5.9).
+// through ctypes, 6.1 here; rope 15.9, 5.9; append 10.3, 4.5; decode 16.0, 5.9).
 // The library stays the C ABI of include/sage.h: its functions are handed over
 // as addresses by the package, which has loaded it.
 #include <Python.h>
