@@ -71,8 +71,12 @@ constexpr int kMinSteps = 2;      // of one warp's stretch
 constexpr float kSlack = 4.f;
 // How many times the unit of O delta_V may be before it follows.
 constexpr float kUnitSlack = 2.f;
-// Where fp16 P stands: 2^15 is the largest it gets.
-constexpr float kLift = 15.f - kSlack, kLiftV = kLift - 1.f;
+// Where fp16 P stands (in log2): 2^15 is the largest it gets.
+constexpr int kLift = 11, kLiftV = 10;
+static_assert(kLift + kSlack == 15.f, "P, a score's lag included");
+static_assert((1 << kLiftV) * kUnitSlack == (1 << kLift), "and P delta_V, the unit's included");
+// of an instantiation; bf16 P needs none
+__host__ __device__ constexpr int lift_of(bool half_p, int format) { return !half_p ? 0 : format == SAGE_KV_8P8 ? kLiftV : kLift; }
 // How much larger the second numbers of small P are, and which are small: a number
 // that is below fp16's normal ones is off by 2^-25, which is 2^-16 of 2^-9.  Below
 // 2^-37 nothing of a P is left either way.
@@ -118,6 +122,7 @@ struct DecodeParams {
   int B, H, Hk, G, n_q, rows, groups;  // rows = G * n_q in `groups` groups of 8 NT
   int max_len, causal, workers, step_tokens, cluster;
   float scale_log2;
+  float up;                      // 2^kUp: how many times too small the O of unfinished pieces is
   uint64_t timeout_ns;
 };
 
@@ -576,7 +581,7 @@ __device__ __forceinline__ void join_cluster(const DecodeParams& p, int b, int h
         [&](int i) { return reinterpret_cast<const float4*>(box) + place * p.cluster + i; });
     const int row = row0 + r, qi = row / p.G;
     const int64_t out = (static_cast<int64_t>(b) * p.H + h * p.G + (row - qi * p.G)) * p.n_q + qi;
-    const float g = f.l > 0.f ? 1.f / f.l : 0.f;
+    const float g = f.l > 0.f ? p.up / f.l : 0.f;
     *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.o) + out * D + ch) =
         make_uint2(pack16<T>(f.o[0] * g, f.o[1] * g), pack16<T>(f.o[2] * g, f.o[3] * g));
     if (p.lse != nullptr && ch == 0)
@@ -592,7 +597,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
   using TV = typename std::conditional<FMT == SAGE_KV_8P8, __half, T>::type;
   constexpr bool kScaledQ = !std::is_same<T, TK>::value;
   constexpr bool kHalfP = std::is_same<TV, __half>::value;
-  constexpr float kUp = !kHalfP ? 0.f : FMT == SAGE_KV_8P8 ? kLiftV : kLift;
+  constexpr float kUp = lift_of(kHalfP, FMT);
   constexpr int ROWS = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t s_full[kWarps * kStages], s_empty[kWarps * kStages];
@@ -973,9 +978,7 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
           if (S::VS) {
             const float f[2] = {vs[u][0] * per_unit, vs[u][1] * per_unit};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              e[i] *= f[i >> 1];
-            }
+            for (int i = 0; i < 4; ++i) e[i] *= f[i >> 1];
           }
           if (kHalfP) {
 #pragma unroll
@@ -1050,6 +1053,9 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
     // Channels of a lane: VE neighbours of each of the VC pieces (a V piece's
     // channels are spread over VE / 2 tiles, two a tile).
     constexpr int TILES = S::VE / 2;
+    // O of an unfinished piece goes without the lift, for which V near bf16's end
+    // leaves no room
+    const float in = unit * (1.f / (1 << lift_of(kHalfP, FMT)));
     // where an unfinished piece goes: the workspace, or the warp's own ring
     const int64_t slot_p = 2 * static_cast<int64_t>(worker_of(warp)) + (first_piece ? 0 : 1);
     float* const part_o = MODE == kCluster ? reinterpret_cast<float*>(ring) : p.part_o + slot_p * ROWS * D;
@@ -1089,8 +1095,8 @@ __global__ void __launch_bounds__((kWarps + kFeeders) * 32, 1) k_attn_decode(con
 #pragma unroll
             for (int i = 0; i < TILES; i += 2)
               *reinterpret_cast<float4*>(dst + x * 8 * S::VE + 2 * i) =
-                  make_float4(acc[n][x * TILES + i][e] * unit, acc[n][x * TILES + i][e + 2] * unit,
-                              acc[n][x * TILES + i + 1][e] * unit, acc[n][x * TILES + i + 1][e + 2] * unit);
+                  make_float4(acc[n][x * TILES + i][e] * in, acc[n][x * TILES + i][e + 2] * in,
+                              acc[n][x * TILES + i + 1][e] * in, acc[n][x * TILES + i + 1][e + 2] * in);
           if (g == 0) part_ml[rg] = make_float2(m[n][e], sum);
         }
       }
@@ -1229,7 +1235,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_attn_join(const DecodeParams p, 
         if (i0 >= n) break;
         load_pieces<D>(x, row, piece, late, i0, 1, n);
       }
-      const float f = l > 0.f ? 1.f / l : 0.f;
+      const float f = l > 0.f ? p.up / l : 0.f;
       const int64_t out = out_of(rg);
       uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(p.o) + out * D + lane * PER);
 #pragma unroll
@@ -1296,7 +1302,7 @@ __global__ void __launch_bounds__(WARPS * 32) k_attn_join(const DecodeParams p, 
         a0 += s_o[w][2 * threadIdx.x];
         a1 += s_o[w][2 * threadIdx.x + 1];
       }
-      const float f = ll > 0.f ? 1.f / ll : 0.f;
+      const float f = ll > 0.f ? p.up / ll : 0.f;
       const int64_t out = out_of(rg);
       reinterpret_cast<uint32_t*>(reinterpret_cast<T*>(p.o) + out * D)[threadIdx.x] = pack16<T>(a0 * f, a1 * f);
       if (p.lse != nullptr && threadIdx.x == 0)
@@ -1452,6 +1458,7 @@ cudaError_t launch_attn_decode(const DecodeArgs& a, cudaStream_t st) {
   p.cluster = P.cluster;
   p.timeout_ns = a.timeout_ns;
   p.scale_log2 = a.sm_scale * 1.4426950408889634f;
+  p.up = static_cast<float>(1 << lift_of(c.dtype == SAGE_F16 || c.format == SAGE_KV_8P8, c.format));
   if (c.dtype == SAGE_F16)
     return c.d == 64 ? launch_d<__half, 64>(p, P, c.format, st) : launch_d<__half, 128>(p, P, c.format, st);
   return c.d == 64 ? launch_d<__nv_bfloat16, 64>(p, P, c.format, st)

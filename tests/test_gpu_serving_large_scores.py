@@ -85,3 +85,20 @@ def test_growing_scores_of_every_size(sage, dtype, fmt, G):
             o = sage.sage_attn_decode_paged(q.to(dtype), c, table, ints([n]), n, sm_scale=1.0)[0].double()
             slack = (u + 2.0 ** -14) * A
             assert bool(((o >= low - slack) & (o <= high + slack)).all()), (big, small)
+
+
+@pytest.mark.parametrize("fmt", ["16", "B", "8+8"])
+@pytest.mark.parametrize("n", [60, 3000, 20000])
+@pytest.mark.parametrize("log2_v", [-90, -60, 100, 110])
+def test_v_of_every_size(sage, fmt, n, log2_v):
+    """bf16 V so large that n of it are just below fp32's largest number, or small,
+    under equal scores: its mean, by the bounds above."""
+    d, G = 64, 3
+    g = torch.Generator(device="cuda").manual_seed(n)
+    k = torch.zeros(1, n, d, dtype=torch.bfloat16, device="cuda")
+    v = ((torch.rand(1, n, d, generator=g, device="cuda") + 1) * 2.0 ** log2_v).bfloat16()
+    c, table, V = filled(sage, k, v, fmt)
+    q = torch.ones(1, G, d, dtype=torch.bfloat16, device="cuda")
+    o = sage.sage_attn_decode_paged(q, c, table, ints([n]), n)[0].double()
+    want = V.mean(1)[0]
+    assert bool(((o - want).abs() <= (2.0 ** -8 + 2.0 ** -16 + 2.0 ** -17) * want).all())
