@@ -49,12 +49,20 @@ def is_stale() -> bool:
     return _older(LIB, _inputs())
 
 
-def _run(cmd, what: str, verbose: bool):
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if verbose or res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-    if res.returncode != 0:
-        raise RuntimeError(f"building {what} failed:\n" + res.stderr[-4000:])
+def _run(cmd, target: str, what: str, verbose: bool):
+    """Run a compiler whose output is `target`.  It appears whole or not at all, also
+    if another process builds it at the same time."""
+    tmp = f"{target}.{os.getpid()}.tmp"
+    try:
+        res = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+        if verbose or res.returncode != 0:
+            sys.stderr.write(res.stdout + res.stderr)
+        if res.returncode != 0:
+            raise RuntimeError(f"building {what} failed:\n" + res.stderr[-4000:])
+        os.replace(tmp, target)
+    finally:
+        if os.path.exists(tmp):
+            os.remove(tmp)
 
 
 def _objects(force: bool, verbose: bool):
@@ -69,8 +77,8 @@ def _objects(force: bool, verbose: bool):
             if not force and not _older(obj, [path, *headers]):
                 continue
             cmd = [_nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"),
-                   *(["-Xptxas", "-v"] if verbose else []), "-c", "-o", obj, path]
-            jobs.append(pool.submit(_run, cmd, source, verbose))
+                   *(["-Xptxas", "-v"] if verbose else []), "-c", path]
+            jobs.append(pool.submit(_run, cmd, obj, source, verbose))
         for j in jobs:
             j.result()
     return objects
@@ -87,11 +95,9 @@ def build_serving(verbose: bool = False, force: bool = False) -> str:
     include = [os.path.join(ROOT, "include"), os.path.join(at, "include"),
                os.path.join(at, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
                sysconfig.get_paths()["include"]]
-    tmp = SERVING + ".tmp"
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-          *[x for i in include for x in ("-I", i)], SERVING_SOURCE, "-o", tmp, "-L", os.path.join(at, "lib"),
-          "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], "_serving.so", verbose)
-    os.replace(tmp, SERVING)
+          *[x for i in include for x in ("-I", i)], SERVING_SOURCE, "-L", os.path.join(at, "lib"),
+          "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], SERVING, "_serving.so", verbose)
     return SERVING
 
 
@@ -99,10 +105,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
     """Compile every CUDA source into libsage.so next to this file, and the
     serving calls' Python side."""
     if force or is_stale():
-        tmp = LIB + ".tmp"
-        _run([_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *_objects(force, verbose)],
-             "libsage.so", verbose)
-        os.replace(tmp, LIB)
+        _run([_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", *_objects(force, verbose)],
+             LIB, "libsage.so", verbose)
     build_serving(verbose, force)
     return LIB
 
