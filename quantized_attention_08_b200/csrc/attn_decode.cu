@@ -8,7 +8,7 @@
 // query heads of its group (and all query tokens).  Measured on one B200,
 // device time with the join: 89 us for one request of 131072 tokens (H 32,
 // H_kv 8, d 128, bf16: 537 MB, 0.92 of the measured copy rate), 93.4 us for 64
-// requests of 1 to 8192 tokens in 8+8 (570 MB, 0.93; 97 to 103 us for seconds on end,
+// requests of 1 to 8192 tokens in 8+8 (570 MB, 0.93; 96 to 103 us for seconds on end,
 // when the power cap lowers the clock).
 //
 // Work.  The cache of one (request, kv head, group of query rows) is a
@@ -44,7 +44,7 @@
 // 2^-46 of the largest P times the largest delta_V).  One number instead of two
 // made the output's error up to 1.5 times that of its own rounding, and lost the keys 17
 // nats below the largest.  64 requests of 8+8 in sequence: 97.5 us fp16, 103 bf16 (99
-// with one number); four drafted tokens, bf16: 43.6 (39.3).
+// with one number); four drafted tokens, bf16: 43.1 (39.3).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>

@@ -193,7 +193,7 @@ cudaError_t launch_kv_slots(const SlotArgs& a, cudaStream_t st) {
 // lanes and its maximum log2(d / 16) shuffles; its loads do not wait for its
 // slot (a skipped token is read for nothing).  One row a thread and six CTAs an
 // SM: 65536 tokens of 8 heads, d 128, fp16 with means, 8+8 (407 MB) take 67 us on the
-// device, 0.93 of the measured copy rate (69 to 72 in sequence, where the power cap
+// device, 0.93 of the measured copy rate (69 to 73 in sequence, where the power cap
 // lowers the clock); two or four rows a thread with the next one's loads in flight
 // took 9 and 27% longer (more registers, fewer warps).
 constexpr int kAppendThreads = 256;
