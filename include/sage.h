@@ -316,7 +316,8 @@ typedef enum {
  * allocation, say) and are multiples of 16 bytes.  k_scale and v_scale are
  * fp32 [num_pages, H_kv, page_size] with their own page strides (16-byte
  * aligned too, strides multiples of 4): K = code * k_scale, V = e4m3 * v_scale
- * (unused ones are ignored and may be NULL).
+ * (unused ones are ignored and may be NULL); a scale is 0 or at least 2^-100, as
+ * sage_kv_append writes it.
  * page_size is a multiple of 16, num_pages * page_size < 2^31.  Slot s is token
  * s % page_size of page s / page_size.
  */
